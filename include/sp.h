@@ -246,6 +246,68 @@ typedef enum {
 sp_status sp_out_projection(const void *o, const void *w, const void *bias, void *y,
                             int32_t hidden, int32_t layout, const sp_shape *shape, void *stream);
 
+/* How layer norm's parameters are laid out, and their element type. */
+typedef enum {
+  SP_PARAM_SHARED = 0,    /* [hidden]: one row for every token */
+  SP_PARAM_PER_SAMPLE = 1 /* [B][hidden]: one row per batch entry */
+} sp_param_layout;
+typedef enum { SP_PARAM_BF16 = 0, SP_PARAM_FP32 = 1 } sp_param_type;
+
+/* Largest hidden size of the layer norm calls. */
+#define SP_NORM_MAX_HIDDEN 8192
+
+/* Layer norm over the hidden state of each token, the step in front of
+ * sp_qkv_projection in a transformer block:
+ *   xh = (x - mean(x)) * rstd,  rstd = 1 / sqrt(var(x) + eps),
+ *   y = xh * weight + bias
+ * with the mean and the (biased) variance over the hidden elements.  The
+ * pages never describe the block around the attention; this is its plainest
+ * reading, with the parameters either shared or per sample (a diffusion
+ * transformer modulates each generation's norm by its own scale and shift).
+ * fp32 arithmetic, one rounding to bf16.  The result does not depend on P.
+ * x: device bf16 [P][B][Nl][hidden], the sequence-sharded hidden states, read
+ *   only; padding slots (tokens at or past N) are not read.  One rank's shard
+ *   [B][Nl][hidden] is the problem {B, Nl, ..., P = 1}.
+ * weight, bias: device parameters of param_layout and param_type, or NULL
+ *   (weight 1, bias 0), each on its own.
+ * y: device bf16, as x, written in full (padding slots +0.0); not x.
+ * mean, rstd: device fp32 [P][B][Nl] for the backward pass, or NULL; written
+ *   in full (padding slots 0).
+ * hidden: a multiple of 8, at most SP_NORM_MAX_HIDDEN.  eps <= 0 selects
+ *   1e-6.  shape: {B, N, H, D, P}; H, D and scale are ignored.
+ * Alignment: 16 bytes; mean and rstd 4 bytes.  Errors: SP_ERR_NULL,
+ * SP_ERR_ALIGN, SP_ERR_SHAPE (sizes, layout, type), SP_ERR_CUDA. */
+sp_status sp_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                        float *rstd, int32_t hidden, float eps, int32_t param_layout,
+                        int32_t param_type, const sp_shape *shape, void *stream);
+
+/* Bytes of the workspace of sp_layer_norm_backward, for either parameter
+ * layout; -1 when the shape or hidden is out of range. */
+int64_t sp_layer_norm_backward_workspace(const sp_shape *shape, int32_t hidden);
+
+/* Backward pass of sp_layer_norm: with g = dy * weight,
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)),
+ *   dweight = sum over the tokens of dy * xh,  dbias = sum over the tokens of dy
+ * (each sample's tokens on their own for SP_PARAM_PER_SAMPLE).  fp32
+ * arithmetic; every sum has a fixed order that depends on neither P nor
+ * timing, so results repeat bit for bit.
+ * dy, x: device bf16 [P][B][Nl][hidden], read only; padding slots are not
+ *   read.  mean, rstd: what the forward call wrote.  weight: as forward.
+ * dx: device bf16, as x, written in full (padding slots +0.0); neither dy
+ *   nor x.
+ * dweight, dbias: device, of param_layout and param_type, written; both or
+ *   neither (frozen parameters).
+ * workspace: device, sp_layer_norm_backward_workspace bytes, contents
+ *   irrelevant before and after; NULL when dweight is.  Calls that may run at
+ *   the same time need one each.
+ * Errors: SP_ERR_NULL (also one of dweight and dbias alone), otherwise as
+ * for sp_layer_norm. */
+sp_status sp_layer_norm_backward(const void *dy, const void *x, const void *weight,
+                                 const float *mean, const float *rstd, void *dx, void *dweight,
+                                 void *dbias, void *workspace, int32_t hidden,
+                                 int32_t param_layout, int32_t param_type, const sp_shape *shape,
+                                 void *stream);
+
 /* Tokens per cube of the block-sparse call's mask, and the most cubes
  * (ceil(N / SP_SPARSE_CUBE)) the call takes: 524,288 tokens. */
 #define SP_SPARSE_CUBE 64

@@ -45,7 +45,8 @@ EXPORTED = ("sp_padded_tokens", "sp_check_shape", "sp_pack", "sp_unpack",
             "sp_attention_ulysses_peer", "sp_ipc_export", "sp_ipc_open", "sp_ipc_close",
             "sp_attention_sparse_seqsharded", "sp_qkv_projection", "sp_out_projection",
             "sp_exchange_push", "sp_attention_ulysses_overlap", "sp_shard", "sp_unshard",
-            "sp_copy_heads")
+            "sp_copy_heads", "sp_layer_norm", "sp_layer_norm_backward",
+            "sp_layer_norm_backward_workspace")
 
 
 class sp_shape(ctypes.Structure):
@@ -92,6 +93,13 @@ def load(path: str = LIB_PATH):
     lib.sp_qkv_projection.restype = ctypes.c_int
     lib.sp_out_projection.argtypes = [vp, vp, vp, vp, ctypes.c_int32, ctypes.c_int32, sp_p, vp]
     lib.sp_out_projection.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    lib.sp_layer_norm.argtypes = [vp] * 6 + [i32, ctypes.c_float, i32, i32, sp_p, vp]
+    lib.sp_layer_norm.restype = ctypes.c_int
+    lib.sp_layer_norm_backward_workspace.argtypes = [sp_p, i32]
+    lib.sp_layer_norm_backward_workspace.restype = ctypes.c_int64
+    lib.sp_layer_norm_backward.argtypes = [vp] * 9 + [i32, i32, i32, sp_p, vp]
+    lib.sp_layer_norm_backward.restype = ctypes.c_int
     lib.sp_attention_sparse_seqsharded.argtypes = [vp, vp, vp, vp, vp, vp, sp_p, vp]
     lib.sp_attention_sparse_seqsharded.restype = ctypes.c_int
     lib.sp_attention_ulysses_peer.argtypes = [
@@ -499,6 +507,104 @@ def out_projection(o, w, bias, y, shape: Shape, layout: str = "seq", stream=None
             _ptr(o, o_shape, "o"), _ptr(w, (hidden, shape.H * shape.D), "w"),
             _ptr(bias, (hidden,), "bias"), _ptr(y, tuple(rows) + (hidden,), "y"), hidden,
             O_LAYOUTS[layout], ctypes.byref(s), _stream(stream, o.device)), "sp_out_projection")
+
+
+NORM_MAX_HIDDEN = 8192   # SP_NORM_MAX_HIDDEN
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """A caller's workspace (any contiguous CUDA tensor of at least nbytes),
+    or a fresh one that belongs to the stream the call runs on, so that its
+    memory is reused in that stream's order."""
+    torch = _torch()
+    if workspace is None:
+        with torch.cuda.stream(stream):   # None: the current stream stays
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
+                         f"{nbytes} needed")
+    return workspace
+
+
+def _norm_params(params, shape: Shape, hidden: int):
+    """(param_layout, param_type, torch dtype, tensor shape) of layer norm's
+    parameters; the given ones must agree."""
+    torch = _torch()
+    given = [t for t in params if t is not None]
+    if not given:
+        return 0, 0, torch.bfloat16, (hidden,)
+    t = given[0]
+    if not all(isinstance(o, torch.Tensor) for o in given):
+        raise TypeError("layer norm parameters must be tensors")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"layer norm parameters must be bfloat16 or float32, got {t.dtype}")
+    pshape = (hidden,) if t.dim() == 1 else (shape.B, hidden)
+    for o in given:
+        if o.dtype != t.dtype or tuple(o.shape) != pshape:
+            raise ValueError(f"layer norm parameters must all be {t.dtype} of shape ({hidden},) or "
+                             f"({shape.B}, {hidden}), got {o.dtype} {tuple(o.shape)}")
+    return int(t.dim() == 2), int(t.dtype == torch.float32), t.dtype, pshape
+
+
+def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: float = 1e-6,
+               stream=None):
+    """Layer norm of the hidden states (sp_layer_norm): x and y bf16
+    [P][B][Nl][hidden]; weight and bias [hidden], or [B][hidden] for a
+    modulation of its own per sample, bf16 or float32, or None; mean and rstd
+    receive the rows' statistics (float32 [P][B][Nl]) for the backward
+    pass."""
+    torch = _torch()
+    hidden = int(x.shape[-1])
+    rows = shape.seq_sharded[:3]
+    layout, ptype, dtype, pshape = _norm_params((weight, bias), shape, hidden)
+    s = shape.c()
+    with _same_device(x, weight, bias, y, mean, rstd):
+        _check(load().sp_layer_norm(
+            _ptr(x, rows + (hidden,), "x"), _ptr(weight, pshape, "weight", dtype),
+            _ptr(bias, pshape, "bias", dtype), _ptr(y, rows + (hidden,), "y"),
+            _ptr(mean, rows, "mean", torch.float32), _ptr(rstd, rows, "rstd", torch.float32),
+            hidden, float(eps), layout, ptype, ctypes.byref(s), _stream(stream, x.device)),
+            "sp_layer_norm")
+
+
+def layer_norm_backward_workspace(shape: Shape, hidden: int) -> int:
+    """Bytes of layer_norm_backward's workspace."""
+    s = shape.c()
+    n = int(load().sp_layer_norm_backward_workspace(ctypes.byref(s), int(hidden)))
+    if n < 0:
+        raise SpError(SP_ERR_SHAPE, "sp_layer_norm_backward_workspace")
+    return n
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=None, dbias=None,
+                        workspace=None, stream=None):
+    """Backward pass of layer_norm (sp_layer_norm_backward): dx receives the
+    gradient of x, dweight and dbias (both or neither; shape and type of the
+    parameters) the sums over the tokens.  workspace: a CUDA tensor of at
+    least layer_norm_backward_workspace bytes to reuse (one per call in
+    flight), else a fresh one."""
+    torch = _torch()
+    hidden = int(x.shape[-1])
+    rows = shape.seq_sharded[:3]
+    layout, ptype, dtype, pshape = _norm_params((weight, dweight, dbias), shape, hidden)
+    s = shape.c()
+    with _same_device(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace):
+        st = _stream(stream, x.device)
+        ws = None
+        if dweight is not None or dbias is not None:
+            ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden), x.device,
+                            stream)
+        _check(load().sp_layer_norm_backward(
+            _ptr(dy, rows + (hidden,), "dy"), _ptr(x, rows + (hidden,), "x"),
+            _ptr(weight, pshape, "weight", dtype), _ptr(mean, rows, "mean", torch.float32),
+            _ptr(rstd, rows, "rstd", torch.float32), _ptr(dx, rows + (hidden,), "dx"),
+            _ptr(dweight, pshape, "dweight", dtype), _ptr(dbias, pshape, "dbias", dtype),
+            None if ws is None else ctypes.c_void_p(ws.data_ptr()), hidden, layout, ptype,
+            ctypes.byref(s), st), "sp_layer_norm_backward")
 
 
 SPARSE_CUBE = 64         # SP_SPARSE_CUBE

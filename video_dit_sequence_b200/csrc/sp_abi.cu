@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -14,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "attention.cuh"
+#include "layer_norm.cuh"
 #include "permute.cuh"
 #include "projection.cuh"
 #include "sp.h"
@@ -727,6 +729,146 @@ sp_status launch_projection(const CUtensorMap &ma, const void *w, int slots, sp:
   return launch_status(e == cudaSuccess ? cudaGetLastError() : e);
 }
 
+// Layer norm (see sp_layer_norm in sp.h).  Only B, N and P of the shape count.
+sp_status check_norm(const sp_shape *s, int32_t hidden, int32_t param_layout, int32_t param_type) {
+  if (s == nullptr) return SP_ERR_NULL;
+  if (s->B < 1 || s->N < 1 || s->P < 1 || s->B > 65535 || s->P > 65535) return SP_ERR_SHAPE;
+  if (hidden < 8 || hidden % 8 != 0 || hidden > SP_NORM_MAX_HIDDEN) return SP_ERR_SHAPE;
+  if (param_layout < SP_PARAM_SHARED || param_layout > SP_PARAM_PER_SAMPLE ||
+      param_type < SP_PARAM_BF16 || param_type > SP_PARAM_FP32)
+    return SP_ERR_SHAPE;
+  const int64_t Nl = (static_cast<int64_t>(s->N) + s->P - 1) / s->P;
+  if (Nl * s->P >= (int64_t(1) << 31) || Nl * s->P * s->B >= (int64_t(1) << 31))
+    return SP_ERR_SHAPE;
+  return SP_OK;
+}
+
+sp::LnParams norm_params(const sp_shape *s, int32_t hidden, int32_t param_layout,
+                         int32_t param_type) {
+  sp::LnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.C8 = hidden / 8;
+  p.P = s->P;
+  p.B = s->B;
+  p.N = s->N;
+  p.Nl = static_cast<int32_t>((static_cast<int64_t>(s->N) + s->P - 1) / s->P);
+  p.rows = static_cast<int64_t>(p.P) * p.B * p.Nl;
+  p.per_sample = param_layout == SP_PARAM_PER_SAMPLE;
+  p.param_f32 = param_type == SP_PARAM_FP32;
+  p.inv_c = 1.0f / static_cast<float>(hidden);
+  return p;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+sp_status layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                     float *rstd, int32_t hidden, float eps, int32_t param_layout,
+                     int32_t param_type, const sp_shape *s, void *stream) {
+  sp_status st = check_norm(s, hidden, param_layout, param_type);
+  if (st != SP_OK) return st;
+  if (x == nullptr || y == nullptr) return SP_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias) ||
+      !aligned4(mean) || !aligned4(rstd))
+    return SP_ERR_ALIGN;
+  sp::LnParams p = norm_params(s, hidden, param_layout, param_type);
+  p.x = static_cast<const uint4 *>(x);
+  p.y = static_cast<uint4 *>(y);
+  p.weight = weight;
+  p.bias = bias;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.eps = eps > 0.f ? eps : 1e-6f;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>((p.rows + sp::kLnFwdWarps - 1) / sp::kLnFwdWarps));
+  const dim3 block(32 * sp::kLnFwdWarps);
+  const int v = (p.C8 + 31) / 32;  // vectors per lane
+  if (v <= 1) sp::layer_norm_kernel<1><<<grid, block, 0, cs>>>(p);
+  else if (v <= 2) sp::layer_norm_kernel<2><<<grid, block, 0, cs>>>(p);
+  else if (v <= 4) sp::layer_norm_kernel<4><<<grid, block, 0, cs>>>(p);
+  else if (v <= 6) sp::layer_norm_kernel<6><<<grid, block, 0, cs>>>(p);
+  else if (v <= 8) sp::layer_norm_kernel<8><<<grid, block, 0, cs>>>(p);
+  else if (v <= 12) sp::layer_norm_kernel<12><<<grid, block, 0, cs>>>(p);
+  else if (v <= 16) sp::layer_norm_kernel<16><<<grid, block, 0, cs>>>(p);
+  else if (v <= 20) sp::layer_norm_kernel<20><<<grid, block, 0, cs>>>(p);
+  else sp::layer_norm_kernel<32><<<grid, block, 0, cs>>>(p);
+  static_assert(SP_NORM_MAX_HIDDEN <= 32 * 32 * 8, "a warp holds a row");
+  return launch_status(cudaGetLastError());
+}
+
+// Threads of a block of the backward pass: one vector of 8 columns each up
+// to 1,024 columns, two above.
+int norm_backward_threads(int C8) {
+  const int per = C8 <= 128 ? 1 : 2;
+  return ((C8 + per - 1) / per + 31) / 32 * 32;
+}
+
+// Most blocks of a group of the backward pass: no fewer than eight rows a
+// block, and at most what 148 SMs hold at 1,024 threads and 16 blocks each,
+// over all groups.  Each block leaves one partial row of both gradients.
+int64_t norm_backward_blocks(int64_t nrows, int64_t groups, int C8) {
+  const int threads = norm_backward_threads(C8);
+  const int64_t cap = 148 * std::max(1, std::min(16, 1024 / threads));
+  const int64_t per_group = std::max<int64_t>(1, cap / groups);
+  return std::min<int64_t>((nrows + 7) / 8, per_group);
+}
+
+int64_t norm_backward_workspace(const sp_shape *s, int32_t hidden) {
+  if (check_norm(s, hidden, SP_PARAM_SHARED, SP_PARAM_BF16) != SP_OK) return -1;
+  const int64_t shared = norm_backward_blocks(static_cast<int64_t>(s->B) * s->N, 1, hidden / 8);
+  const int64_t sample = s->B * norm_backward_blocks(s->N, s->B, hidden / 8);
+  return std::max(shared, sample) * 2 * hidden * 4;
+}
+
+template <int V, bool kGrad>
+cudaError_t launch_norm_backward(const sp::LnParams &p, int64_t blocks, int groups, int threads,
+                                 cudaStream_t cs) {
+  sp::layer_norm_backward_kernel<V, kGrad>
+      <<<dim3(static_cast<unsigned>(blocks), groups), threads, 0, cs>>>(p);
+  return cudaGetLastError();
+}
+
+sp_status layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                              const float *rstd, void *dx, void *dweight, void *dbias,
+                              void *workspace, int32_t hidden, int32_t param_layout,
+                              int32_t param_type, const sp_shape *s, void *stream) {
+  sp_status st = check_norm(s, hidden, param_layout, param_type);
+  if (st != SP_OK) return st;
+  if (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr)
+    return SP_ERR_NULL;
+  const bool grad = dweight != nullptr;
+  if (grad != (dbias != nullptr) || (grad && workspace == nullptr)) return SP_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(weight) || !aligned16(dx) ||
+      !aligned16(dweight) || !aligned16(dbias) || !aligned16(workspace) || !aligned4(mean) ||
+      !aligned4(rstd))
+    return SP_ERR_ALIGN;
+  sp::LnParams p = norm_params(s, hidden, param_layout, param_type);
+  p.x = static_cast<const uint4 *>(x);
+  p.dy = static_cast<const uint4 *>(dy);
+  p.y = static_cast<uint4 *>(dx);
+  p.weight = weight;
+  p.mean_in = mean;
+  p.rstd_in = rstd;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.partial = static_cast<float *>(workspace);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int groups = p.per_sample ? p.B : 1;
+  const int64_t nrows = p.per_sample ? p.N : static_cast<int64_t>(p.B) * p.N;
+  const int64_t blocks = norm_backward_blocks(nrows, groups, p.C8);
+  const int threads = norm_backward_threads(p.C8);
+  const bool one = p.C8 <= threads;
+  const cudaError_t e = one ? (grad ? launch_norm_backward<1, true>(p, blocks, groups, threads, cs)
+                                    : launch_norm_backward<1, false>(p, blocks, groups, threads, cs))
+                            : (grad ? launch_norm_backward<2, true>(p, blocks, groups, threads, cs)
+                                    : launch_norm_backward<2, false>(p, blocks, groups, threads, cs));
+  st = launch_status(e);
+  if (st != SP_OK || !grad) return st;
+  const dim3 grid((hidden + sp::kLnGradCols - 1) / sp::kLnGradCols, groups, 2);
+  sp::layer_norm_grad_kernel<<<grid, sp::kLnGradCols * sp::kLnGradRows, 0, cs>>>(
+      p, static_cast<int>(blocks));
+  return launch_status(cudaGetLastError());
+}
+
 using AddressRangeFn = CUresult (*)(CUdeviceptr *, size_t *, CUdeviceptr);
 
 AddressRangeFn address_range_fn() {
@@ -888,6 +1030,28 @@ sp_status sp_out_projection(const void *o, const void *w, const void *bias, void
                             int32_t hidden, int32_t layout, const sp_shape *shape, void *stream) {
   NvtxRange range("sp_out_projection");
   return out_projection(o, w, bias, y, hidden, layout, shape, stream);
+}
+
+sp_status sp_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                        float *rstd, int32_t hidden, float eps, int32_t param_layout,
+                        int32_t param_type, const sp_shape *shape, void *stream) {
+  NvtxRange range("sp_layer_norm");
+  return layer_norm(x, weight, bias, y, mean, rstd, hidden, eps, param_layout, param_type, shape,
+                    stream);
+}
+
+int64_t sp_layer_norm_backward_workspace(const sp_shape *shape, int32_t hidden) {
+  return norm_backward_workspace(shape, hidden);
+}
+
+sp_status sp_layer_norm_backward(const void *dy, const void *x, const void *weight,
+                                 const float *mean, const float *rstd, void *dx, void *dweight,
+                                 void *dbias, void *workspace, int32_t hidden,
+                                 int32_t param_layout, int32_t param_type, const sp_shape *shape,
+                                 void *stream) {
+  NvtxRange range("sp_layer_norm_backward");
+  return layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, hidden,
+                             param_layout, param_type, shape, stream);
 }
 
 sp_status sp_attention_ulysses_peer(const void *const *q_shards, const void *k_group,
