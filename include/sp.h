@@ -246,6 +246,41 @@ typedef enum {
 sp_status sp_out_projection(const void *o, const void *w, const void *bias, void *y,
                             int32_t hidden, int32_t layout, const sp_shape *shape, void *stream);
 
+/* Bytes of the workspace of the attention backward calls, for either layout;
+ * -1 when the shape is out of range.  About 4 B H N (D + 2) bytes, or
+ * ceil(N / 128) times that for short sequences that fill the GPU once. */
+int64_t sp_attention_backward_workspace(const sp_shape *shape);
+
+/* Backward pass of sp_attention: with P_ik = exp(scale q_i.k_k - lse_i) over
+ * the N true tokens, delta_i = sum_c dO_ic O_ic and
+ * dS_ik = P_ik (dO_i.v_k - delta_i),
+ *   dQ_i = scale sum_k dS_ik k_k, dK_k = scale sum_i dS_ik q_i,
+ *   dV_k = sum_i P_ik dO_i.
+ * The probabilities are recomputed; P and dS are rounded to bf16 for the
+ * tensor core, every sum is fp32, each gradient is rounded once.  Results
+ * repeat bit for bit and do not depend on P or the layout.
+ * q, k, v, o, d_o: device bf16 [P][B][Np][Hl][D]: the inputs and the output of
+ *   the forward call and the output's gradient, read only; padding slots are
+ *   not used, whatever they hold.
+ * lse: device fp32 [B][H][Np], as the forward call wrote it; a row of -inf
+ *   has no key and gets no gradient.
+ * dq, dk, dv: device bf16, as q, written in full (padding slots +0.0);
+ *   distinct, and none of the inputs.
+ * workspace: device, sp_attention_backward_workspace bytes, contents
+ *   irrelevant before and after.  Calls that may run at the same time need one
+ *   each.
+ * Alignment: 16 bytes; lse 4 bytes.  Errors as for sp_attention. */
+sp_status sp_attention_backward(const void *q, const void *k, const void *v, const void *o,
+                                const float *lse, const void *d_o, void *dq, void *dk, void *dv,
+                                void *workspace, const sp_shape *shape, void *stream);
+
+/* The same on sequence-sharded tensors [P][B][Nl][H][D]: the backward pass of
+ * sp_attention_seqsharded, for any P. */
+sp_status sp_attention_backward_seqsharded(const void *q, const void *k, const void *v,
+                                           const void *o, const float *lse, const void *d_o,
+                                           void *dq, void *dk, void *dv, void *workspace,
+                                           const sp_shape *shape, void *stream);
+
 /* How layer norm's parameters are laid out, and their element type. */
 typedef enum {
   SP_PARAM_SHARED = 0,    /* [hidden]: one row for every token */

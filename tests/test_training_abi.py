@@ -72,3 +72,39 @@ def test_layer_norm_workspace(lib):
         assert n == sp.layer_norm_backward_workspace(sp.Shape(B, N, 1, 128, 4), C)
     with pytest.raises(sp.SpError):
         sp.layer_norm_backward_workspace(sp.Shape(1, 10, 1, 128, 1), 60)
+
+
+def _attn_back(lib, seq=True, shape=sp.Shape(1, 10, 2, 128, 2), **kw):
+    a = {n: A for n in ("q", "k", "v", "o", "lse", "do", "dq", "dk", "dv", "ws")}
+    a.update(kw)
+    s = shape.c() if shape is not None else None
+    fn = lib.sp_attention_backward_seqsharded if seq else lib.sp_attention_backward
+    return fn(*[_p(v) for v in a.values()], ctypes.byref(s) if s is not None else None, None)
+
+
+@pytest.mark.parametrize("seq", [True, False])
+def test_attention_backward_refusals(lib, seq):
+    names = ("q", "k", "v", "o", "lse", "do", "dq", "dk", "dv", "ws")
+    for n in names:
+        assert _attn_back(lib, seq, **{n: 0}) == sp.SP_ERR_NULL
+        assert _attn_back(lib, seq, **{n: A + 2}) == sp.SP_ERR_ALIGN
+        if n != "lse":
+            assert _attn_back(lib, seq, **{n: A + 8}) == sp.SP_ERR_ALIGN
+    assert _attn_back(lib, seq, shape=None) == sp.SP_ERR_NULL
+    assert _attn_back(lib, seq, shape=sp.Shape(1, 10, 2, 96, 2)) == sp.SP_ERR_UNSUPPORTED_D
+    for s in (sp.Shape(0, 10, 2, 128, 2), sp.Shape(1, 0, 2, 128, 2), sp.Shape(1, 10, 0, 128, 2),
+              sp.Shape(1, 10, 2, 128, 0), sp.Shape(1, 2 ** 30, 16, 128, 2)):
+        assert _attn_back(lib, seq, shape=s) == sp.SP_ERR_SHAPE
+    if not seq:
+        assert _attn_back(lib, seq, shape=sp.Shape(1, 10, 3, 128, 2)) == sp.SP_ERR_HEADS_NOT_DIVISIBLE
+
+
+def test_attention_backward_workspace(lib):
+    for B, N, H, D in ((1, 1, 1, 64), (2, 777, 6, 128), (1, 4096, 40, 128), (1, 75600, 40, 128)):
+        n = sp.attention_backward_workspace(sp.Shape(B, N, H, D, 1))
+        tiles = -(-N // 128)
+        # the fp32 dQ and two statistics a row at least
+        assert n >= B * H * tiles * 128 * 4 * (D + 2)
+        assert n == sp.attention_backward_workspace(sp.Shape(B, N, H, D, 5))
+    with pytest.raises(sp.SpError):
+        sp.attention_backward_workspace(sp.Shape(1, 10, 1, 32, 1))

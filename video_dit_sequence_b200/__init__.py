@@ -46,7 +46,8 @@ EXPORTED = ("sp_padded_tokens", "sp_check_shape", "sp_pack", "sp_unpack",
             "sp_attention_sparse_seqsharded", "sp_qkv_projection", "sp_out_projection",
             "sp_exchange_push", "sp_attention_ulysses_overlap", "sp_shard", "sp_unshard",
             "sp_copy_heads", "sp_layer_norm", "sp_layer_norm_backward",
-            "sp_layer_norm_backward_workspace")
+            "sp_layer_norm_backward_workspace", "sp_attention_backward",
+            "sp_attention_backward_seqsharded", "sp_attention_backward_workspace")
 
 
 class sp_shape(ctypes.Structure):
@@ -100,6 +101,11 @@ def load(path: str = LIB_PATH):
     lib.sp_layer_norm_backward_workspace.restype = ctypes.c_int64
     lib.sp_layer_norm_backward.argtypes = [vp] * 9 + [i32, i32, i32, sp_p, vp]
     lib.sp_layer_norm_backward.restype = ctypes.c_int
+    for fn in (lib.sp_attention_backward, lib.sp_attention_backward_seqsharded):
+        fn.argtypes = [vp] * 10 + [sp_p, vp]
+        fn.restype = ctypes.c_int
+    lib.sp_attention_backward_workspace.argtypes = [sp_p]
+    lib.sp_attention_backward_workspace.restype = ctypes.c_int64
     lib.sp_attention_sparse_seqsharded.argtypes = [vp, vp, vp, vp, vp, vp, sp_p, vp]
     lib.sp_attention_sparse_seqsharded.restype = ctypes.c_int
     lib.sp_attention_ulysses_peer.argtypes = [
@@ -507,6 +513,51 @@ def out_projection(o, w, bias, y, shape: Shape, layout: str = "seq", stream=None
             _ptr(o, o_shape, "o"), _ptr(w, (hidden, shape.H * shape.D), "w"),
             _ptr(bias, (hidden,), "bias"), _ptr(y, tuple(rows) + (hidden,), "y"), hidden,
             O_LAYOUTS[layout], ctypes.byref(s), _stream(stream, o.device)), "sp_out_projection")
+
+
+def attention_backward_workspace(shape: Shape) -> int:
+    """Bytes of the workspace of attention_backward and
+    attention_backward_seqsharded."""
+    s = shape.c()
+    n = int(load().sp_attention_backward_workspace(ctypes.byref(s)))
+    if n < 0:
+        raise SpError(SP_ERR_SHAPE, "sp_attention_backward_workspace")
+    return n
+
+
+def _attention_backward(name, ts, q, k, v, o, lse, do, dq, dk, dv, shape, workspace, stream):
+    torch = _torch()
+    s = shape.c()
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"),
+                 (dk, "dk"), (dv, "dv"), (q if workspace is None else workspace, "workspace")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a CUDA tensor")
+    with _same_device(q, k, v, o, lse, do, dq, dk, dv, workspace):
+        st = _stream(stream, q.device)
+        ws = _workspace(workspace, attention_backward_workspace(shape), q.device, stream)
+        _check(getattr(load(), name)(
+            _ptr(q, ts, "q"), _ptr(k, ts, "k"), _ptr(v, ts, "v"), _ptr(o, ts, "o"),
+            _ptr(lse, shape.lse_shape, "lse", torch.float32), _ptr(do, ts, "do"),
+            _ptr(dq, ts, "dq"), _ptr(dk, ts, "dk"), _ptr(dv, ts, "dv"),
+            ctypes.c_void_p(ws.data_ptr()), ctypes.byref(s), st), name)
+
+
+def attention_backward(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None, stream=None):
+    """Backward pass of attention on head-sharded tensors: from the forward
+    call's inputs, output and lse and the output's gradient do, the gradients
+    dq, dk and dv.  workspace: a CUDA tensor of at least
+    attention_backward_workspace bytes to reuse (one per call in flight), else
+    a fresh one."""
+    _attention_backward("sp_attention_backward", shape.head_sharded, q, k, v, o, lse, do, dq, dk,
+                        dv, shape, workspace, stream)
+
+
+def attention_backward_seqsharded(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None,
+                                  stream=None):
+    """Backward pass of attention_seqsharded on sequence-sharded tensors;
+    arguments as for attention_backward."""
+    _attention_backward("sp_attention_backward_seqsharded", shape.seq_sharded, q, k, v, o, lse, do,
+                        dq, dk, dv, shape, workspace, stream)
 
 
 NORM_MAX_HIDDEN = 8192   # SP_NORM_MAX_HIDDEN

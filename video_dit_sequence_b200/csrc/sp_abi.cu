@@ -15,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "attention.cuh"
+#include "attention_backward.cuh"
 #include "layer_norm.cuh"
 #include "permute.cuh"
 #include "projection.cuh"
@@ -869,6 +870,120 @@ sp_status layer_norm_backward(const void *dy, const void *x, const void *weight,
   return launch_status(cudaGetLastError());
 }
 
+// Backward pass of attention (see sp_attention_backward in sp.h).
+
+// Every key tile writes its own partial dQ when all of them run at once and a
+// head has few: see kMaxPartial's comment at attention_backward_plan.
+constexpr int kMaxPartialTiles = 16;
+// Heads whose key tiles run at the same time.
+constexpr int kBackwardHeadGroup = 8;
+
+struct BackwardPlan {
+  int T, BH;
+  bool partial;
+  int64_t dq_acc, stat, turn, bytes;  // byte sizes of the workspace's parts, total
+};
+
+BackwardPlan backward_plan(const sp_shape *s) {
+  BackwardPlan pl;
+  pl.T = (s->N + 127) / 128;
+  pl.BH = s->B * s->H;
+  const int64_t tiles = static_cast<int64_t>(pl.BH) * pl.T;
+  pl.partial = pl.T <= kMaxPartialTiles && tiles <= 148;
+  pl.dq_acc = tiles * (pl.partial ? pl.T : 1) * 128 * s->D * 4;
+  pl.stat = tiles * 128 * 4;
+  pl.turn = (tiles * 16 + 8 + 255) / 256 * 256;
+  pl.bytes = pl.dq_acc + 2 * pl.stat + pl.turn;
+  return pl;
+}
+
+template <int D>
+sp_status launch_attention_backward(const CUtensorMap *m, const sp::AttnBwdParams &p,
+                                    cudaStream_t cs) {
+  using C = sp::AttnBwdCfg<D>;
+  static bool attr_set[kMaxDevices] = {};
+  if (set_smem_once(sp::attention_backward_kernel<D>, C::kSmemBytes, attr_set) != cudaSuccess)
+    return SP_ERR_CUDA;
+  const unsigned tiles = static_cast<unsigned>(p.BH) * p.T;
+  sp::attention_delta_kernel<D><<<tiles, 256, 0, cs>>>(p);
+  sp_status st = launch_status(cudaGetLastError());
+  if (st != SP_OK) return st;
+  sp::attention_backward_kernel<D><<<tiles, C::kThreads, C::kSmemBytes, cs>>>(m[0], m[1], m[2],
+                                                                              m[3], p);
+  st = launch_status(cudaGetLastError());
+  if (st != SP_OK) return st;
+  const unsigned pad = static_cast<unsigned>(p.BH) * (p.Np - p.N);
+  sp::attention_dq_kernel<D><<<tiles + pad, 256, 0, cs>>>(p);
+  return launch_status(cudaGetLastError());
+}
+
+sp_status attention_backward(const void *q, const void *k, const void *v, const void *o,
+                             const float *lse, const void *d_o, void *dq, void *dk, void *dv,
+                             void *workspace, const sp_shape *s, void *stream, bool seqsharded) {
+  sp_status st = check_common(s, !seqsharded);
+  if (st != SP_OK) return st;
+  if (q == nullptr || k == nullptr || v == nullptr || o == nullptr || lse == nullptr ||
+      d_o == nullptr || dq == nullptr || dk == nullptr || dv == nullptr || workspace == nullptr)
+    return SP_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(d_o) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace) ||
+      !aligned4(lse))
+    return SP_ERR_ALIGN;
+  const int P = s->P, B = s->B, H = s->H, D = s->D, N = s->N;
+  const int Hl = H / P;
+  const int Nl = (N + P - 1) / P;
+  const int Np = Nl * P;
+  const bool rank_major = seqsharded && B > 1 && P > 1;
+  const int Hx = seqsharded ? H : Hl;
+  const int Bx = seqsharded ? B : P * B;
+  const int64_t row_el = static_cast<int64_t>(Hx) * D;
+  const int64_t batch_el = static_cast<int64_t>(seqsharded ? Nl : Np) * Hx * D;
+  int32_t *status = status_ptr();
+  if (status == nullptr) return SP_ERR_CUDA;
+  CUtensorMap m[4];
+  const void *src[4] = {q, k, v, d_o};
+  for (int i = 0; i < 4; ++i)
+    if (!(rank_major ? make_map5(&m[i], src[i], D, H, Nl, B, P)
+                     : make_map(&m[i], src[i], D, Hx, N, Bx, row_el, batch_el)))
+      return SP_ERR_CUDA;
+  const BackwardPlan pl = backward_plan(s);
+  sp::AttnBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.N = N;
+  p.Np = Np;
+  p.H = H;
+  p.B = B;
+  p.hsplit = Hx;
+  p.T = pl.T;
+  p.BH = pl.BH;
+  p.head_group = std::min(pl.BH, kBackwardHeadGroup);
+  p.partial = pl.partial;
+  p.nl_split = rank_major ? Nl : 0;
+  p.scale = s->scale > 0.f ? s->scale : 1.0f / std::sqrt(static_cast<float>(D));
+  p.scale_log2e = p.scale * 1.4426950408889634f;
+  p.q = static_cast<const uint8_t *>(q);
+  p.k = static_cast<const uint8_t *>(k);
+  p.v = static_cast<const uint8_t *>(v);
+  p.o = static_cast<const uint8_t *>(o);
+  p.dout = static_cast<const uint8_t *>(d_o);
+  p.lse = lse;
+  p.dq = static_cast<__nv_bfloat16 *>(dq);
+  p.dk = static_cast<__nv_bfloat16 *>(dk);
+  p.dv = static_cast<__nv_bfloat16 *>(dv);
+  p.row_el = row_el;
+  p.batch_el = batch_el;
+  p.rank_el = static_cast<int64_t>(B) * Nl * H * D;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.dq_acc = reinterpret_cast<float *>(ws);
+  p.ndelta = reinterpret_cast<float *>(ws + pl.dq_acc);
+  p.nlse2 = reinterpret_cast<float *>(ws + pl.dq_acc + pl.stat);
+  p.turn = reinterpret_cast<uint32_t *>(ws + pl.dq_acc + 2 * pl.stat);
+  p.ticket = p.turn + static_cast<int64_t>(pl.BH) * pl.T * 4;
+  p.status = status;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return D == 64 ? launch_attention_backward<64>(m, p, cs) : launch_attention_backward<128>(m, p, cs);
+}
+
 using AddressRangeFn = CUresult (*)(CUdeviceptr *, size_t *, CUdeviceptr);
 
 AddressRangeFn address_range_fn() {
@@ -1052,6 +1167,26 @@ sp_status sp_layer_norm_backward(const void *dy, const void *x, const void *weig
   NvtxRange range("sp_layer_norm_backward");
   return layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, hidden,
                              param_layout, param_type, shape, stream);
+}
+
+int64_t sp_attention_backward_workspace(const sp_shape *shape) {
+  if (check_common(shape, false) != SP_OK) return -1;
+  return backward_plan(shape).bytes;
+}
+
+sp_status sp_attention_backward(const void *q, const void *k, const void *v, const void *o,
+                                const float *lse, const void *d_o, void *dq, void *dk, void *dv,
+                                void *workspace, const sp_shape *shape, void *stream) {
+  NvtxRange range("sp_attention_backward");
+  return attention_backward(q, k, v, o, lse, d_o, dq, dk, dv, workspace, shape, stream, false);
+}
+
+sp_status sp_attention_backward_seqsharded(const void *q, const void *k, const void *v,
+                                           const void *o, const float *lse, const void *d_o,
+                                           void *dq, void *dk, void *dv, void *workspace,
+                                           const sp_shape *shape, void *stream) {
+  NvtxRange range("sp_attention_backward_seqsharded");
+  return attention_backward(q, k, v, o, lse, d_o, dq, dk, dv, workspace, shape, stream, true);
 }
 
 sp_status sp_attention_ulysses_peer(const void *const *q_shards, const void *k_group,
