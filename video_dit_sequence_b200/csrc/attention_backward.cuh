@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 
 #include "attention.cuh"
+#include "projection.cuh"
 #include "sm100.cuh"
 
 namespace sp {
@@ -65,7 +66,7 @@ struct AttnBwdParams {
   __nv_bfloat16 *dq, *dk, *dv;
   int64_t row_el, batch_el, rank_el;  // strides of tokens, slots, rank slabs
   // workspace
-  float *dq_acc;         // [BH][T][key tiles or 1][D / 4][128] float4
+  float *dq_acc;         // [BH][T][key tiles or 1][4 x 32 rows][D / 32][8][32 rows] float4
   float *ndelta;         // [BH][128 T]: -delta, 0 past N
   float *nlse2;          // [BH][128 T]: -lse * log2(e), -inf past N
   uint32_t *turn;        // [BH][T][4]: key tiles that added their part
@@ -138,9 +139,12 @@ struct AttnBwdCfg {
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kTileBytes;
   static constexpr int kOffQ = 2 * kTileBytes;        // two stages
-  static constexpr int kOffDO = 4 * kTileBytes;       // two stages
-  static constexpr int kOffDS = 6 * kTileBytes;       // [2 query halves][128 keys][128 bytes]
-  static constexpr int kOffStat = kOffDS + 2 * kBlockBytes;  // [2 stages][nlse2, ndelta][128]
+  static constexpr int kOffDO = 4 * kTileBytes;       // one stage
+  static constexpr int kOffDS = 5 * kTileBytes;       // [2 query halves][128 keys][128 bytes]
+  // dQ on its way out: [4 warps][2 buffers][32 rows x 32 columns] fp32
+  static constexpr int kChunkBytes = 32 * 32 * 4;
+  static constexpr int kOffOut = kOffDS + 2 * kBlockBytes;
+  static constexpr int kOffStat = kOffOut + 8 * kChunkBytes;  // [2 stages][nlse2, ndelta][128]
   static constexpr int kOffBar = kOffStat + 2 * 2 * 512;
   static constexpr int kNumBar = 20;
   static constexpr int kOffMisc = kOffBar + kNumBar * 8;  // TMEM base, abort flag, work item
@@ -161,11 +165,42 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu_u32(const uint32_t *p) {
 __device__ __forceinline__ void st_release_gpu_u32(uint32_t *p, uint32_t v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-__device__ __forceinline__ void red_add_v4(float4 *p, const uint32_t *r) {
-  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1,%2,%3,%4};"
-               ::"l"(p), "f"(__uint_as_float(r[0])), "f"(__uint_as_float(r[1])),
-                 "f"(__uint_as_float(r[2])), "f"(__uint_as_float(r[3]))
+// Bulk copies shared -> global in this thread's groups (16-byte aligned,
+// multiples of 16 bytes): a plain store, or fp32 adds performed in L2.
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+               ::"l"(dst), "r"(src), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void bulk_add_f32(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;"
+               ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+// Matrix products of bf16 operands whose descriptors differ from one another
+// only in the low word: high word = stride 1,024 bytes, version 1, 128-byte
+// swizzle (make_sdesc_sw128).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void umma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
 }
 
 // Untiled bulk copy global -> shared (16-byte aligned, multiple of 16 bytes).
@@ -195,7 +230,7 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   const uint32_t bar_k = sbase + C::kOffBar, bar_v = bar_k + 8;
   const uint32_t bar_q_full = bar_k + 16, bar_q_empty = bar_k + 32;
-  const uint32_t bar_do_full = bar_k + 48, bar_do_empty = bar_k + 64;
+  const uint32_t bar_do_full = bar_k + 48, bar_do_empty = bar_k + 56;
   const uint32_t bar_s = bar_k + 80;
   const uint32_t bar_p = bar_k + 88;    // [2]
   const uint32_t bar_dp = bar_k + 104;
@@ -217,11 +252,11 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_q_full + 8 * s, 1);
       mbar_init(bar_q_empty + 8 * s, 1);
-      mbar_init(bar_do_full + 8 * s, 1);
-      mbar_init(bar_do_empty + 8 * s, 1);
       mbar_init(bar_p + 8 * s, 128);
       mbar_init(bar_ds + 8 * s, 128);
     }
+    mbar_init(bar_do_full, 1);
+    mbar_init(bar_do_empty, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_dp, 1);
     mbar_init(bar_dq, 1);
@@ -331,13 +366,12 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
           load(&tmV, p.v, sbase + C::kOffV, bar_v, k0, pol_kv, false, 0);
           kv_issued = true;
         }
-        got = mbar_wait(bar_do_empty + 8 * s, free_par, abort_flag, kWaitLimitNs);
+        got = mbar_wait(bar_do_empty, (j & 1) ^ 1, abort_flag, kWaitLimitNs);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        load(&tmDO, p.dout, sbase + C::kOffDO + s * C::kTileBytes, bar_do_full + 8 * s, j * 128,
-             pol_q, false, 0);
+        load(&tmDO, p.dout, sbase + C::kOffDO, bar_do_full, j * 128, pol_q, false, 0);
         issued = 2 * j + 2;
       }
     } else if (warp == 13) {
@@ -346,74 +380,77 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
         constexpr uint32_t idesc_kk = make_idesc_bf16(128, 128, 0, 0);  // S^T, dP^T
         constexpr uint32_t idesc_acc = make_idesc_bf16(128, D, 0, 1);   // dV, dK
         constexpr uint32_t idesc_dq = make_idesc_bf16(128, D, 1, 1);    // dQ
-        const uint64_t dK_k = make_sdesc_sw128(sbase + C::kOffK, 16, 1024);
-        const uint64_t dV_k = make_sdesc_sw128(sbase + C::kOffV, 16, 1024);
-        const uint64_t dQ_k = make_sdesc_sw128(sbase + C::kOffQ, 16, 1024);
-        const uint64_t dDO_k = make_sdesc_sw128(sbase + C::kOffDO, 16, 1024);
-        const uint64_t dK_mn = make_sdesc_sw128(sbase + C::kOffK, C::kBlockBytes, 1024);
-        const uint64_t dQ_mn = make_sdesc_sw128(sbase + C::kOffQ, C::kBlockBytes, 1024);
-        const uint64_t dDO_mn = make_sdesc_sw128(sbase + C::kOffDO, C::kBlockBytes, 1024);
-        const uint64_t dDS_mn = make_sdesc_sw128(sbase + C::kOffDS, C::kBlockBytes, 1024);
+        // Descriptors are kept as their low words (start address, leading
+        // offset); the high word is one constant.  With 64-bit descriptors
+        // this warp's share of registers spilled, and its reloads waited
+        // behind the dQ warps' reductions in the load/store unit: 22.1
+        // instead of TODO ms at 480p.
+        constexpr uint32_t kLboK = 1u << 16;                               // K-major: unused
+        constexpr uint32_t kLboMn = static_cast<uint32_t>(C::kBlockBytes >> 4) << 16;
+        const uint32_t s16 = sbase >> 4;
         constexpr uint32_t kStage = C::kTileBytes >> 4;
         // [128 x 128] = A B^T over D, both operands K-major
-        auto issue_kk = [&](uint32_t d, uint64_t a, uint64_t bb) {
+        auto issue_kk = [&](uint32_t d, uint32_t a, uint32_t bb) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-            umma_ss(d, a + off, bb + off, idesc_kk, kk > 0 ? 1u : 0u);
+            umma_ss_lo(d, a + (off | kLboK), bb + (off | kLboK), idesc_kk, kk > 0 ? 1u : 0u);
           }
         };
         // acc += X[:, 64h .. 64h+63] B[64h .. 64h+63, :], X in tensor memory
-        auto issue_acc = [&](uint32_t d, uint32_t x, uint64_t bb, int h, bool first) {
+        auto issue_acc = [&](uint32_t d, uint32_t x, uint32_t bb, int h, bool first) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_ts(d, x + 64 * h + 8 * k, bb + static_cast<uint32_t>(((4 * h + k) * 16 * 128) >> 4),
-                    idesc_acc, (first && h == 0 && k == 0) ? 0u : 1u);
+            umma_ts_lo(d, x + 64 * h + 8 * k, bb + (((4 * h + k) * 16 * 128) >> 4) + kLboMn, idesc_acc,
+                       (first && h == 0 && k == 0) ? 0u : 1u);
         };
+        const uint32_t aK = s16 + (C::kOffK >> 4), aV = s16 + (C::kOffV >> 4);
+        const uint32_t aQ = s16 + (C::kOffQ >> 4), aDO = s16 + (C::kOffDO >> 4);
+        const uint32_t aDS = s16 + (C::kOffDS >> 4);
         const uint32_t R0 = tmem, R1 = tmem + C::kColR1;
         ok = mbar_wait(bar_k, 0, abort_flag, kWaitLimitNs) &&
              mbar_wait(bar_q_full, 0, abort_flag, kWaitLimitNs);
         if (ok) {
           tc_fence_after();
-          issue_kk(R0, dK_k, dQ_k);
+          issue_kk(R0, aK, aQ);
           umma_commit(bar_s);
           ok = mbar_wait(bar_v, 0, abort_flag, kWaitLimitNs);
         }
         for (int j = 0; j < T && ok; ++j) {
           const int s = j & 1;
-          const uint32_t par = j & 1, spar = (j >> 1) & 1;
-          ok = mbar_wait(bar_do_full + 8 * s, spar, abort_flag, kWaitLimitNs);
+          const uint32_t par = j & 1;
+          ok = mbar_wait(bar_do_full, par, abort_flag, kWaitLimitNs);
           for (int h = 0; h < 2 && ok; ++h) {
             ok = mbar_wait(bar_p + 8 * h, par, abort_flag, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            issue_acc(tmem + C::kColDV, R0, dDO_mn + s * kStage, h, j == 0);
+            issue_acc(tmem + C::kColDV, R0, aDO, h, j == 0);
           }
           if (ok && j > 0) ok = mbar_wait(bar_dq_free, par ^ 1u, abort_flag, kWaitLimitNs);
           if (!ok) break;
           tc_fence_after();
-          issue_kk(R1, dV_k, dDO_k + s * kStage);
+          issue_kk(R1, aV, aDO);
           umma_commit(bar_dp);
-          umma_commit(bar_do_empty + 8 * s);
+          umma_commit(bar_do_empty);
           if (j + 1 < T) {
             ok = mbar_wait(bar_q_full + 8 * (s ^ 1), ((j + 1) >> 1) & 1, abort_flag, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            issue_kk(R0, dK_k, dQ_k + (s ^ 1) * kStage);
+            issue_kk(R0, aK, aQ + (s ^ 1) * kStage);
             umma_commit(bar_s);
           }
           for (int h = 0; h < 2 && ok; ++h) {
             ok = mbar_wait(bar_ds + 8 * h, par, abort_flag, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            issue_acc(tmem + C::kColDK, R1, dQ_mn + s * kStage, h, j == 0);
+            issue_acc(tmem + C::kColDK, R1, aQ + s * kStage, h, j == 0);
           }
           if (!ok) break;
           umma_commit(bar_q_empty + 8 * s);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk * 16 * 128) >> 4;
-            umma_ss(R1, dDS_mn + off, dK_mn + off, idesc_dq, kk > 0 ? 1u : 0u);
+            umma_ss_lo(R1, aDS + off + kLboMn, aK + off + kLboMn, idesc_dq, kk > 0 ? 1u : 0u);
           }
           umma_commit(bar_dq);
         }
@@ -427,28 +464,40 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int wq = warp & 3;
     const uint32_t tR1 = tmem + (static_cast<uint32_t>(wq * 32) << 16) + C::kColR1;
     const int parts = p.partial ? T : 1;
-    float4 *acc = reinterpret_cast<float4 *>(p.dq_acc) +
-                  (static_cast<int64_t>(bh) * T * parts + (p.partial ? n : 0)) * (D / 4) * 128 +
-                  wq * 32 + lane;
+    constexpr int kChunks = D / 32;
+    // this warp's 32 rows of the head's accumulators, query tile 0
+    uint8_t *acc = reinterpret_cast<uint8_t *>(p.dq_acc) +
+                   ((static_cast<int64_t>(bh) * T * parts + (p.partial ? n : 0)) * 4 + wq) *
+                       (kChunks * C::kChunkBytes);
+    const int64_t acc_tile = static_cast<int64_t>(parts) * 4 * kChunks * C::kChunkBytes;
     uint32_t *turn = p.turn + static_cast<int64_t>(bh) * T * 4 + wq;
-    const bool ordered = !p.partial && n > 0;
-    for (int j = 0; j < T; ++j) {
-      const bool got = mbar_wait(bar_dq, j & 1, abort_flag, kWaitLimitNs);
-      if (!__all_sync(0xffffffffu, got)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+    const bool add = !p.partial && n > 0, pass = !p.partial && n + 1 < T;
+    const uint32_t buf = sbase + C::kOffOut + wq * 2 * C::kChunkBytes;
+    for (int j = 0; j <= T; ++j) {
       uint32_t r[D];
+      if (j < T) {
+        const bool got = mbar_wait(bar_dq, j & 1, abort_flag, kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < D; c += 32) tmem_ld32(tR1 + c, r + c);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(bar_dq_free);
-      float4 *dst = acc + static_cast<int64_t>(j) * parts * (D / 4) * 128;
-      if (ordered) {
-        bool mine = true;
-        if (lane == 0) {
+        for (int c = 0; c < D; c += 32) tmem_ld32(tR1 + c, r + c);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar_dq_free);
+      }
+      // The tile before this one has had an iteration to reach L2: wait until
+      // its adds are complete and pass its turn on.
+      bool mine = true;
+      if (lane == 0) {
+        bulk_wait_all();
+        if (pass && j > 0) {
+          fence_proxy_async_global();
+          st_release_gpu_u32(turn + 4 * (j - 1), static_cast<uint32_t>(n + 1));
+        }
+        if (add && j < T) {
           if (ld_acquire_gpu_u32(turn + 4 * j) < static_cast<uint32_t>(n)) {
             const uint64_t t0 = globaltimer_ns();
             while (ld_acquire_gpu_u32(turn + 4 * j) < static_cast<uint32_t>(n)) {
@@ -459,25 +508,37 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
               }
             }
           }
+          fence_proxy_async_global();
         }
-        if (!__all_sync(0xffffffffu, mine)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int c = 0; c < D / 4; ++c) red_add_v4(dst + c * 128, r + 4 * c);
-      } else {
-#pragma unroll
-        for (int c = 0; c < D / 4; ++c)
-          dst[c * 128] = make_float4(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]),
-                                     __uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
       }
-      if (!p.partial && n + 1 < T) {
-        __threadfence();
+      if (!__all_sync(0xffffffffu, mine)) {
+        ok = false;
+        break;
+      }
+      if (j == T) break;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const uint32_t dst = buf + (c & 1) * C::kChunkBytes;
+        if (c >= 2) {  // the buffer's last copy has been read
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4(dst + i * 512 + lane * 16,
+                       make_uint4(r[32 * c + 4 * i], r[32 * c + 4 * i + 1], r[32 * c + 4 * i + 2],
+                                  r[32 * c + 4 * i + 3]));
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) st_release_gpu_u32(turn + 4 * j, static_cast<uint32_t>(n + 1));
+        if (lane == 0) {
+          uint8_t *g_dst = acc + j * acc_tile + c * C::kChunkBytes;
+          if (add) bulk_add_f32(g_dst, dst, C::kChunkBytes);
+          else bulk_store(g_dst, dst, C::kChunkBytes);
+          bulk_commit();
+        }
       }
     }
+    if (lane == 0) bulk_wait_all();  // no copy outlives the CTA's shared memory
   } else {
     // ---------------------------------------------------------------- elementwise
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
@@ -615,8 +676,7 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int nq = (issued + 1) >> 1, ndo = issued >> 1;  // loads issued
       for (int j = max(nq - 2, 0); j < nq; ++j)
         mbar_wait_drain(bar_q_full + 8 * (j & 1), (j >> 1) & 1, kWaitLimitNs);
-      for (int j = max(ndo - 2, 0); j < ndo; ++j)
-        mbar_wait_drain(bar_do_full + 8 * (j & 1), (j >> 1) & 1, kWaitLimitNs);
+      if (ndo > 0) mbar_wait_drain(bar_do_full, (ndo - 1) & 1, kWaitLimitNs);
     }
     if (warp == 13 && lane == 0) {
       umma_commit(bar_drain);
@@ -656,16 +716,17 @@ __global__ void __launch_bounds__(256) attention_dq_kernel(const __grid_constant
                       static_cast<int64_t>(blockIdx.x) * parts * (D / 4) * 128;
   const int row = threadIdx.x & 127, t = qt * 128 + row;
   if (t >= p.N) return;
+  src += (row >> 5) * (D / 4) * 32 + (row & 31);
   uint4 *dst = reinterpret_cast<uint4 *>(p.dq + bwd_row(p, bh, t, D));
 #pragma unroll
   for (int c = threadIdx.x >> 7; c < D / 16; c += 2) {
     float4 a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = src[(4 * c + i) * 128 + row];
+    for (int i = 0; i < 4; ++i) a[i] = src[(4 * c + i) * 32];
     for (int k = 1; k < parts; ++k) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = src[static_cast<int64_t>(k) * (D / 4) * 128 + (4 * c + i) * 128 + row];
+        const float4 v = src[static_cast<int64_t>(k) * (D / 4) * 128 + (4 * c + i) * 32];
         a[i].x += v.x, a[i].y += v.y, a[i].z += v.z, a[i].w += v.w;
       }
     }
