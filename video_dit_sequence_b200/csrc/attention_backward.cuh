@@ -28,9 +28,9 @@
 // Tensor memory (512 columns): R0 = 0..127 holds S^T, then P^T; R1 = 128..255
 // holds dP^T, then dS^T, then dQ; dV at 256, dK at 256 + D.  Per query tile j
 // the MMA thread issues
-//   dV += P_j^T dO_j,  dP_j,  S_{j+1},  dK += dS_j^T Q_j,  dQ_j
-// so that the elementwise work on dS_j runs beside S_{j+1}, the exponentials
-// of S_{j+1} beside dK and dQ, and the dQ tile leaves R1 during the next dV.
+//   dP_j,  dV += P_j^T dO_j,  S_{j+1},  dK += dS_j^T Q_j,  dQ_j
+// so that the elementwise work on dS_j runs beside dV and S_{j+1}, and the
+// exponentials of S_{j+1} beside dK, dQ and the dQ tile's way out of R1.
 //
 // dQ_i sums over all keys, i.e. over CTAs.  The key tiles of a head add into
 // the fp32 accumulators in key order, each tile passing a per-(query tile,
@@ -45,6 +45,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "projection.cuh"
@@ -157,6 +158,12 @@ struct AttnBwdCfg {
   static constexpr uint32_t kTmemCols = 512;
 };
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint32_t ld_acquire_gpu_u32(const uint32_t *p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -177,6 +184,12 @@ __device__ __forceinline__ void bulk_add_f32(void *dst, uint32_t src, uint32_t b
                ::"l"(dst), "r"(src), "r"(bytes)
                : "memory");
 }
+// Waits until at most kPending of this thread's bulk groups are incomplete.
+template <int kPending>
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // Matrix products of bf16 operands whose descriptors differ from one another
 // only in the low word: high word = stride 1,024 bytes, version 1, 128-byte
 // swizzle (make_sdesc_sw128).
@@ -230,7 +243,7 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   const uint32_t bar_k = sbase + C::kOffBar, bar_v = bar_k + 8;
   const uint32_t bar_q_full = bar_k + 16, bar_q_empty = bar_k + 32;
-  const uint32_t bar_do_full = bar_k + 48, bar_do_empty = bar_k + 56;
+  const uint32_t bar_do_full = bar_k + 48, bar_dv = bar_k + 56;
   const uint32_t bar_s = bar_k + 80;
   const uint32_t bar_p = bar_k + 88;    // [2]
   const uint32_t bar_dp = bar_k + 104;
@@ -256,13 +269,13 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       mbar_init(bar_ds + 8 * s, 128);
     }
     mbar_init(bar_do_full, 1);
-    mbar_init(bar_do_empty, 1);
+    mbar_init(bar_dv, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_dp, 1);
     mbar_init(bar_dq, 1);
     mbar_init(bar_dq_free, 128);
     mbar_init(bar_acc, 1);
-    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -287,8 +300,9 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
   const int k0 = n * 128;
 
   bool ok = true;
-  int issued = 0;  // query tiles whose Q (low bit 0) and dO loads were issued: 2 j + ...
+  int issued = 0;  // loads of query tiles issued: Q_0, dO_0, Q_1, ...
   bool kv_issued = false;
+  bool leader = false;   // the lanes of warps 13 and 14 that issue MMAs
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12) {
@@ -366,7 +380,9 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
           load(&tmV, p.v, sbase + C::kOffV, bar_v, k0, pol_kv, false, 0);
           kv_issued = true;
         }
-        got = mbar_wait(bar_do_empty, (j & 1) ^ 1, abort_flag, kWaitLimitNs);
+        // dV and dP of the tile before have both read the stage
+        got = j == 0 || (mbar_wait(bar_dv, s ^ 1, abort_flag, kWaitLimitNs) &&
+                         mbar_wait(bar_dp, s ^ 1, abort_flag, kWaitLimitNs));
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
@@ -374,87 +390,97 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
         load(&tmDO, p.dout, sbase + C::kOffDO, bar_do_full, j * 128, pol_q, false, 0);
         issued = 2 * j + 2;
       }
-    } else if (warp == 13) {
+    } else if (warp < 15) {
       // -------------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        constexpr uint32_t idesc_kk = make_idesc_bf16(128, 128, 0, 0);  // S^T, dP^T
-        constexpr uint32_t idesc_acc = make_idesc_bf16(128, D, 0, 1);   // dV, dK
-        constexpr uint32_t idesc_dq = make_idesc_bf16(128, D, 1, 1);    // dQ
-        // Descriptors are kept as their low words (start address, leading
-        // offset); the high word is one constant.  With 64-bit descriptors
-        // this warp's share of registers spilled, and its reloads waited
-        // behind the dQ warps' reductions in the load/store unit: 22.1
-        // instead of TODO ms at 480p.
-        constexpr uint32_t kLboK = 1u << 16;                               // K-major: unused
-        constexpr uint32_t kLboMn = static_cast<uint32_t>(C::kBlockBytes >> 4) << 16;
-        const uint32_t s16 = sbase >> 4;
-        constexpr uint32_t kStage = C::kTileBytes >> 4;
+      // Warp 13 issues the products that feed the elementwise warps, warp 14
+      // those that they feed.  The whole warp runs the loop and one elected
+      // lane issues, and every address is a constant or warp-uniform (the
+      // kernel holds all of tensor memory, so its base is 0), so that
+      // descriptors stay in uniform registers.
+      constexpr uint32_t idesc_kk = make_idesc_bf16(128, 128, 0, 0);  // S^T, dP^T
+      constexpr uint32_t idesc_acc = make_idesc_bf16(128, D, 0, 1);   // dV, dK
+      constexpr uint32_t idesc_dq = make_idesc_bf16(128, D, 1, 1);    // dQ
+      // Low descriptor words: start address / 16 and the leading offset.
+      constexpr uint32_t kLboK = 1u << 16;                               // K-major: unused
+      constexpr uint32_t kLboMn = static_cast<uint32_t>(C::kBlockBytes >> 4) << 16;
+      constexpr uint32_t R0 = 0, R1 = C::kColR1;
+      constexpr uint32_t kStage = C::kTileBytes >> 4;
+      const uint32_t s16 = sbase >> 4;
+      const uint32_t aK = s16 + (C::kOffK >> 4), aV = s16 + (C::kOffV >> 4);
+      const uint32_t aQ = s16 + (C::kOffQ >> 4), aDO = s16 + (C::kOffDO >> 4);
+      const uint32_t aDS = s16 + (C::kOffDS >> 4);
+      leader = elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool got = mbar_wait(bar, parity, abort_flag, kWaitLimitNs);
+        tc_fence_after();
+        return __all_sync(0xffffffffu, got) != 0;
+      };
+      ok = tmem == 0;
+      if (warp == 13) {
         // [128 x 128] = A B^T over D, both operands K-major
         auto issue_kk = [&](uint32_t d, uint32_t a, uint32_t bb) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-            umma_ss_lo(d, a + (off | kLboK), bb + (off | kLboK), idesc_kk, kk > 0 ? 1u : 0u);
+            const uint32_t off = (((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4) | kLboK;
+            umma_ss_lo(d, a + off, bb + off, idesc_kk, kk > 0 ? 1u : 0u);
           }
         };
-        // acc += X[:, 64h .. 64h+63] B[64h .. 64h+63, :], X in tensor memory
-        auto issue_acc = [&](uint32_t d, uint32_t x, uint32_t bb, int h, bool first) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_ts_lo(d, x + 64 * h + 8 * k, bb + (((4 * h + k) * 16 * 128) >> 4) + kLboMn, idesc_acc,
-                       (first && h == 0 && k == 0) ? 0u : 1u);
-        };
-        const uint32_t aK = s16 + (C::kOffK >> 4), aV = s16 + (C::kOffV >> 4);
-        const uint32_t aQ = s16 + (C::kOffQ >> 4), aDO = s16 + (C::kOffDO >> 4);
-        const uint32_t aDS = s16 + (C::kOffDS >> 4);
-        const uint32_t R0 = tmem, R1 = tmem + C::kColR1;
-        ok = mbar_wait(bar_k, 0, abort_flag, kWaitLimitNs) &&
-             mbar_wait(bar_q_full, 0, abort_flag, kWaitLimitNs);
-        if (ok) {
-          tc_fence_after();
-          issue_kk(R0, aK, aQ);
-          umma_commit(bar_s);
-          ok = mbar_wait(bar_v, 0, abort_flag, kWaitLimitNs);
-        }
+        ok = ok && wait(bar_k, 0);
         for (int j = 0; j < T && ok; ++j) {
           const int s = j & 1;
-          const uint32_t par = j & 1;
-          ok = mbar_wait(bar_do_full, par, abort_flag, kWaitLimitNs);
-          for (int h = 0; h < 2 && ok; ++h) {
-            ok = mbar_wait(bar_p + 8 * h, par, abort_flag, kWaitLimitNs);
-            if (!ok) break;
-            tc_fence_after();
-            issue_acc(tmem + C::kColDV, R0, aDO, h, j == 0);
-          }
-          if (ok && j > 0) ok = mbar_wait(bar_dq_free, par ^ 1u, abort_flag, kWaitLimitNs);
+          // R0 is free when dV has used the tile's probabilities
+          ok = wait(bar_q_full + 8 * s, (j >> 1) & 1) && (j == 0 || wait(bar_dv, s ^ 1));
           if (!ok) break;
-          tc_fence_after();
-          issue_kk(R1, aV, aDO);
-          umma_commit(bar_dp);
-          umma_commit(bar_do_empty);
-          if (j + 1 < T) {
-            ok = mbar_wait(bar_q_full + 8 * (s ^ 1), ((j + 1) >> 1) & 1, abort_flag, kWaitLimitNs);
-            if (!ok) break;
-            tc_fence_after();
-            issue_kk(R0, aK, aQ + (s ^ 1) * kStage);
+          if (leader) {
+            issue_kk(R0, aK, aQ + s * kStage);
             umma_commit(bar_s);
           }
-          for (int h = 0; h < 2 && ok; ++h) {
-            ok = mbar_wait(bar_ds + 8 * h, par, abort_flag, kWaitLimitNs);
-            if (!ok) break;
-            tc_fence_after();
-            issue_acc(tmem + C::kColDK, R1, aQ + s * kStage, h, j == 0);
-          }
+          // R1 is free when the tile's dQ has left it
+          ok = (j > 0 || wait(bar_v, 0)) && wait(bar_do_full, s) &&
+               (j == 0 || wait(bar_dq_free, s ^ 1));
           if (!ok) break;
-          umma_commit(bar_q_empty + 8 * s);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk * 16 * 128) >> 4;
-            umma_ss_lo(R1, aDS + off + kLboMn, aK + off + kLboMn, idesc_dq, kk > 0 ? 1u : 0u);
+          if (leader) {
+            issue_kk(R1, aV, aDO);
+            umma_commit(bar_dp);
           }
-          umma_commit(bar_dq);
         }
-        if (ok) umma_commit(bar_acc);
+      } else {
+        // acc += X[:, 64h .. 64h+63] B[64h .. 64h+63, :], X in tensor memory
+        auto issue_acc = [&](uint32_t d, uint32_t x, uint32_t bb, int h, uint32_t more) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_ts_lo(d, x + 64 * h + 8 * k, bb + ((((4 * h + k) * 16 * 128) >> 4) | kLboMn),
+                       idesc_acc, (h == 0 && k == 0) ? more : 1u);
+        };
+        for (int j = 0; j < T && ok; ++j) {
+          const int s = j & 1;
+          const uint32_t par = s, more = j > 0 ? 1u : 0u;
+          ok = wait(bar_do_full, par) && wait(bar_p, par);
+          if (!ok) break;
+          if (leader) issue_acc(C::kColDV, R0, aDO, 0, more);
+          ok = wait(bar_p + 8, par);
+          if (!ok) break;
+          if (leader) {
+            issue_acc(C::kColDV, R0, aDO, 1, 1u);
+            umma_commit(bar_dv);
+          }
+          ok = wait(bar_ds, par);
+          if (!ok) break;
+          if (leader) issue_acc(C::kColDK, R1, aQ + s * kStage, 0, more);
+          ok = wait(bar_ds + 8, par);
+          if (!ok) break;
+          if (leader) {
+            issue_acc(C::kColDK, R1, aQ + s * kStage, 1, 1u);
+            umma_commit(bar_q_empty + 8 * s);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = ((kk * 16 * 128) >> 4) | kLboMn;
+              umma_ss_lo(R1, aDS + off, aK + off, idesc_dq, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(bar_dq);
+          }
+        }
+        if (ok && leader) umma_commit(bar_acc);
       }
       __syncwarp();
     }
@@ -473,56 +499,49 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
     uint32_t *turn = p.turn + static_cast<int64_t>(bh) * T * 4 + wq;
     const bool add = !p.partial && n > 0, pass = !p.partial && n + 1 < T;
     const uint32_t buf = sbase + C::kOffOut + wq * 2 * C::kChunkBytes;
-    for (int j = 0; j <= T; ++j) {
-      uint32_t r[D];
-      if (j < T) {
-        const bool got = mbar_wait(bar_dq, j & 1, abort_flag, kWaitLimitNs);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D; c += 32) tmem_ld32(tR1 + c, r + c);
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bar_dq_free);
+    // Tile j's adds are complete: pass its turn on.
+    auto release = [&](int j) {
+      fence_proxy_async_global();
+      st_release_gpu_u32(turn + 4 * j, static_cast<uint32_t>(n + 1));
+    };
+    for (int j = 0; j < T; ++j) {
+      // asked for before the tile is there, so that the answer's way is hidden
+      uint32_t seen = add && lane == 0 ? ld_acquire_gpu_u32(turn + 4 * j) : 0u;
+      const bool got = mbar_wait(bar_dq, j & 1, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
       }
-      // The tile before this one has had an iteration to reach L2: wait until
-      // its adds are complete and pass its turn on.
+      tc_fence_after();
+      uint32_t r[D];
+#pragma unroll
+      for (int c = 0; c < D; c += 32) tmem_ld32(tR1 + c, r + c);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(bar_dq_free);
       bool mine = true;
-      if (lane == 0) {
-        bulk_wait_all();
-        if (pass && j > 0) {
-          fence_proxy_async_global();
-          st_release_gpu_u32(turn + 4 * (j - 1), static_cast<uint32_t>(n + 1));
-        }
-        if (add && j < T) {
-          if (ld_acquire_gpu_u32(turn + 4 * j) < static_cast<uint32_t>(n)) {
-            const uint64_t t0 = globaltimer_ns();
-            while (ld_acquire_gpu_u32(turn + 4 * j) < static_cast<uint32_t>(n)) {
-              if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs ||
-                  ld_acquire_gpu_u32(p.ticket + 1) != 0u) {
-                mine = false;
-                break;
-              }
+      if (add && lane == 0) {
+        if (seen < static_cast<uint32_t>(n)) {
+          const uint64_t t0 = globaltimer_ns();
+          while (ld_acquire_gpu_u32(turn + 4 * j) < static_cast<uint32_t>(n)) {
+            if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs ||
+                ld_acquire_gpu_u32(p.ticket + 1) != 0u) {
+              mine = false;
+              break;
             }
           }
-          fence_proxy_async_global();
         }
+        fence_proxy_async_global();
       }
       if (!__all_sync(0xffffffffu, mine)) {
         ok = false;
         break;
       }
-      if (j == T) break;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const uint32_t dst = buf + (c & 1) * C::kChunkBytes;
-        if (c >= 2) {  // the buffer's last copy has been read
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-        }
+        if (lane == 0) bulk_wait_read<1>();  // the buffer's last copy has been read
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           st_shared_v4(dst + i * 512 + lane * 16,
@@ -535,10 +554,18 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (add) bulk_add_f32(g_dst, dst, C::kChunkBytes);
           else bulk_store(g_dst, dst, C::kChunkBytes);
           bulk_commit();
+          if (c == 1 && pass && j > 0) {
+            bulk_wait<2>();  // all but this tile's two chunks
+            release(j - 1);
+          }
         }
       }
     }
-    if (lane == 0) bulk_wait_all();  // no copy outlives the CTA's shared memory
+    if (lane == 0) {
+      bulk_wait_all();  // (no copy outlives the CTA's shared memory either)
+      if (ok && pass) release(T - 1);
+    }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------------- elementwise
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
@@ -678,7 +705,7 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
         mbar_wait_drain(bar_q_full + 8 * (j & 1), (j >> 1) & 1, kWaitLimitNs);
       if (ndo > 0) mbar_wait_drain(bar_do_full, (ndo - 1) & 1, kWaitLimitNs);
     }
-    if (warp == 13 && lane == 0) {
+    if (leader) {
       umma_commit(bar_drain);
       mbar_wait_drain(bar_drain, 0, kWaitLimitNs);
     }
