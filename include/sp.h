@@ -247,8 +247,7 @@ sp_status sp_out_projection(const void *o, const void *w, const void *bias, void
                             int32_t hidden, int32_t layout, const sp_shape *shape, void *stream);
 
 /* Bytes of the workspace of the attention backward calls, for either layout;
- * -1 when the shape is out of range.  About 4 B H N (D + 2) bytes, or
- * ceil(N / 128) times that for short sequences that fill the GPU once. */
+ * -1 when the shape is out of range: 8 bytes a row of scores. */
 int64_t sp_attention_backward_workspace(const sp_shape *shape);
 
 /* Backward pass of sp_attention: with P_ik = exp(scale q_i.k_k - lse_i) over

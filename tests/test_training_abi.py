@@ -103,8 +103,8 @@ def test_attention_backward_workspace(lib):
     for B, N, H, D in ((1, 1, 1, 64), (2, 777, 6, 128), (1, 4096, 40, 128), (1, 75600, 40, 128)):
         n = sp.attention_backward_workspace(sp.Shape(B, N, H, D, 1))
         tiles = -(-N // 128)
-        # the fp32 dQ and two statistics a row at least
-        assert n >= B * H * tiles * 128 * 4 * (D + 2)
+        # two statistics a row at least
+        assert n >= B * H * tiles * 128 * 8
         assert n == sp.attention_backward_workspace(sp.Shape(B, N, H, D, 5))
     with pytest.raises(sp.SpError):
         sp.attention_backward_workspace(sp.Shape(1, 10, 1, 32, 1))

@@ -872,29 +872,9 @@ sp_status layer_norm_backward(const void *dy, const void *x, const void *weight,
 
 // Backward pass of attention (see sp_attention_backward in sp.h).
 
-// Every key tile writes its own partial dQ when all of them run at once and a
-// head has few: see kMaxPartial's comment at attention_backward_plan.
-constexpr int kMaxPartialTiles = 16;
-// Heads whose key tiles run at the same time.
-constexpr int kBackwardHeadGroup = 8;
-
-struct BackwardPlan {
-  int T, BH;
-  bool partial;
-  int64_t dq_acc, stat, turn, bytes;  // byte sizes of the workspace's parts, total
-};
-
-BackwardPlan backward_plan(const sp_shape *s) {
-  BackwardPlan pl;
-  pl.T = (s->N + 127) / 128;
-  pl.BH = s->B * s->H;
-  const int64_t tiles = static_cast<int64_t>(pl.BH) * pl.T;
-  pl.partial = pl.T <= kMaxPartialTiles && tiles <= 148;
-  pl.dq_acc = tiles * (pl.partial ? pl.T : 1) * 128 * s->D * 4;
-  pl.stat = tiles * 128 * 4;
-  pl.turn = (tiles * 16 + 8 + 255) / 256 * 256;
-  pl.bytes = pl.dq_acc + 2 * pl.stat + pl.turn;
-  return pl;
+// Its workspace: two fp32 statistics per row, in tiles of 128 rows.
+int64_t backward_workspace(const sp_shape *s) {
+  return static_cast<int64_t>(s->B) * s->H * ((s->N + 127) / 128) * 1024;
 }
 
 template <int D>
@@ -905,15 +885,13 @@ sp_status launch_attention_backward(const CUtensorMap *m, const sp::AttnBwdParam
   if (set_smem_once(sp::attention_backward_kernel<D>, C::kSmemBytes, attr_set) != cudaSuccess)
     return SP_ERR_CUDA;
   const unsigned tiles = static_cast<unsigned>(p.BH) * p.T;
-  sp::attention_delta_kernel<D><<<tiles, 256, 0, cs>>>(p);
+  const unsigned pad = static_cast<unsigned>(p.BH) * (p.Np - p.N);
+  sp::attention_delta_kernel<D><<<tiles + pad, 256, 0, cs>>>(p);
   sp_status st = launch_status(cudaGetLastError());
   if (st != SP_OK) return st;
-  sp::attention_backward_kernel<D><<<tiles, C::kThreads, C::kSmemBytes, cs>>>(m[0], m[1], m[2],
-                                                                              m[3], p);
-  st = launch_status(cudaGetLastError());
-  if (st != SP_OK) return st;
-  const unsigned pad = static_cast<unsigned>(p.BH) * (p.Np - p.N);
-  sp::attention_dq_kernel<D><<<tiles + pad, 256, 0, cs>>>(p);
+  const unsigned ctas = static_cast<unsigned>(p.BH) * (p.T + (p.T + 1) / 2);
+  sp::attention_backward_kernel<D><<<ctas, C::kThreads, C::kSmemBytes, cs>>>(m[0], m[1], m[2], m[3],
+                                                                             p);
   return launch_status(cudaGetLastError());
 }
 
@@ -946,7 +924,6 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
     if (!(rank_major ? make_map5(&m[i], src[i], D, H, Nl, B, P)
                      : make_map(&m[i], src[i], D, Hx, N, Bx, row_el, batch_el)))
       return SP_ERR_CUDA;
-  const BackwardPlan pl = backward_plan(s);
   sp::AttnBwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.N = N;
@@ -954,10 +931,8 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
   p.H = H;
   p.B = B;
   p.hsplit = Hx;
-  p.T = pl.T;
-  p.BH = pl.BH;
-  p.head_group = std::min(pl.BH, kBackwardHeadGroup);
-  p.partial = pl.partial;
+  p.T = (N + 127) / 128;
+  p.BH = B * H;
   p.nl_split = rank_major ? Nl : 0;
   p.scale = s->scale > 0.f ? s->scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.scale_log2e = p.scale * 1.4426950408889634f;
@@ -973,12 +948,7 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
   p.row_el = row_el;
   p.batch_el = batch_el;
   p.rank_el = static_cast<int64_t>(B) * Nl * H * D;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  p.dq_acc = reinterpret_cast<float *>(ws);
-  p.ndelta = reinterpret_cast<float *>(ws + pl.dq_acc);
-  p.nlse2 = reinterpret_cast<float *>(ws + pl.dq_acc + pl.stat);
-  p.turn = reinterpret_cast<uint32_t *>(ws + pl.dq_acc + 2 * pl.stat);
-  p.ticket = p.turn + static_cast<int64_t>(pl.BH) * pl.T * 4;
+  p.stat = static_cast<float *>(workspace);
   p.status = status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return D == 64 ? launch_attention_backward<64>(m, p, cs) : launch_attention_backward<128>(m, p, cs);
@@ -1171,7 +1141,7 @@ sp_status sp_layer_norm_backward(const void *dy, const void *x, const void *weig
 
 int64_t sp_attention_backward_workspace(const sp_shape *shape) {
   if (check_common(shape, false) != SP_OK) return -1;
-  return backward_plan(shape).bytes;
+  return backward_workspace(shape);
 }
 
 sp_status sp_attention_backward(const void *q, const void *k, const void *v, const void *o,
