@@ -21,11 +21,12 @@
 //           bf16 for the tensor core as the forward pass rounds P, are the A
 //           operands of dV += P^T dO and dK += dS^T Q from tensor memory.
 //   dQ:     two tiles of 128 queries, which take turns at each 128-key tile
-//           (one K, V load serves both); dS is the A operand of dQ += dS K.
+//           (one K, V load serves both), or one when that still leaves SMs
+//           free; dS is the A operand of dQ += dS K.
 // Roles (12 warps):
 //   warps 0-7   elementwise: warpgroup h takes columns 64h .. 64h+63 of a tile,
 //               one thread per row (key, or query for dQ)
-//   warp 8      TMA producer
+//   warps 8, 10 TMA producers, one per operand pair
 //   warp 9      TMEM allocator and the single MMA-issuing warp
 // Tensor memory (512 columns): R0 = 0..127 scores, then P^T (dK, dV only);
 // R1 = 128..255 dP, then dS; two accumulators from 256.  MMAs of one thread run
@@ -48,6 +49,7 @@ struct AttnBwdParams {
   int32_t hsplit;        // heads per tensor-map "batch" slot (Hl or H)
   int32_t T;             // tiles of 128 tokens
   int32_t BH;            // B * H
+  int32_t dq_tiles;      // query tiles of a dQ CTA: 1 or 2
   int32_t nl_split;      // as in AttnParams
   float scale, scale_log2e;
   const uint8_t *q, *k, *v, *o, *dout;
@@ -169,6 +171,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
       : "memory");
 }
 
+// Asynchronous 16-byte copy global -> shared; bytes = 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+// All of this thread's cp_async16 are complete.
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -270,22 +282,24 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int T2 = (T + 1) / 2;
+  const int T2 = (T + p.dq_tiles - 1) / p.dq_tiles;
   const int bh = blockIdx.x / (T + T2), item = blockIdx.x - bh * (T + T2);
   const bool is_dq = item < T2;
-  const int t0 = is_dq ? item * 256 : (item - T2) * 128;  // first own token
-  const int nt = is_dq && t0 + 128 < p.N ? 2 : 1;         // own tiles
+  const int t0 = is_dq ? item * p.dq_tiles * 128 : (item - T2) * 128;  // first own token
+  const int nt = is_dq && p.dq_tiles == 2 && t0 + 128 < p.N ? 2 : 1;
   const int b = bh / p.H, hg = bh - b * p.H;
 
   bool ok = true;
   bool leader = false;   // the lane of warp 9 that issues MMAs
-  // loads issued by warp 8: own tiles, tiles of the X and Y rings, statistics
-  int n_own = 0, n_x = 0, n_y = 0, n_stat = 0;
-  const int nx = is_dq ? 2 : 3, ny = is_dq ? 1 : 2;       // stages of the rings
+  // loads issued by a producer warp: own tiles, tiles of its ring, statistics
+  int n_own = 0, n_ring = 0, n_stat = 0;
+  const int stages = (is_dq ? 1 : 2) + (warp == 8 ? 1 : 0);  // of its ring
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
-      // -------------------------------------------------------------- producer
+    if (warp == 8 || warp == 10) {
+      // -------------------------------------------------------------- producers
+      // Warp 8: K, the Q ring and the statistics; for dQ the Q tiles and the
+      // K ring.  Warp 10: V and the dO ring; for dQ the dO tiles and V.
       const int hs = hg / p.hsplit;
       const int map_head = hg - hs * p.hsplit, map_batch = hs * p.B + b;
       const uint64_t pol_own = policy_evict_first(), pol_ring = policy_evict_last();
@@ -303,17 +317,29 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int r0 = tok / nl;
         return tok - r0 * nl + 128 <= nl && tok + 128 <= p.N;
       };
-      // The swizzled layout of copy_rows, inlined: the call's registers would
-      // not be held to this warpgroup's share.
+      // 16-byte chunk cc of row r at chunk cc ^ (r mod 8) of its column block,
+      // as the TMA writes it.  Asynchronous copies keep the whole tile in
+      // flight; with loads through registers, four at a time, a tile took
+      // 6 us (777 tokens in 3 shards, 2 x 6 heads: 220 instead of TODO us).
       auto copy_tile = [&](const uint8_t *base, uint32_t dst, int tok) {
-        constexpr int kChunks = D / 8;
+        constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+        const int cc = lane % kChunks;
+        const uint32_t col = dst + (cc >> 3) * C::kBlockBytes;
+        int n = tok + lane / kChunks;                  // token, then its local row
+        const int rk = n / nl;
+        n -= rk * nl;
+        const uint8_t *src = base + cc * 16 +
+                             2 * (rk * p.rank_el + b * p.batch_el + n * p.row_el +
+                                  static_cast<int64_t>(map_head) * D);
+        const int64_t step = 2 * kStep * p.row_el, wrap = 2 * (p.rank_el - nl * p.row_el);
 #pragma unroll 4
-        for (int idx = lane; idx < 128 * kChunks; idx += 32) {
-          const int r = idx / kChunks, cc = idx % kChunks;
-          uint4 val = make_uint4(0u, 0u, 0u, 0u);
-          if (tok + r < p.N) val = ld_global_nc_v4(base + bwd_row(p, bh, tok + r, D) * 2 + cc * 16);
-          st_shared_v4(dst + (cc >> 3) * C::kBlockBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4), val);
+        for (int r = lane / kChunks; r < 128; r += kStep) {
+          const bool in = tok + r < p.N;
+          cp_async16(col + r * 128 + (((cc & 7) ^ (r & 7)) << 4), in ? src : base, in ? 16 : 0);
+          src += step;
+          for (n += kStep; n >= nl; n -= nl) src += wrap;
         }
+        cp_async_wait();
         fence_proxy_async_smem();
       };
       auto load = [&](const CUtensorMap *m, const uint8_t *base, uint32_t dst, uint32_t bar, int tok,
@@ -340,45 +366,40 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs)) != 0;
       };
-      const CUtensorMap *mO = is_dq ? &tmQ : &tmK, *mP = is_dq ? &tmDO : &tmV;  // own tiles
-      const CUtensorMap *mX = is_dq ? &tmK : &tmQ, *mY = is_dq ? &tmV : &tmDO;  // rings
-      const uint8_t *gO = is_dq ? p.q : p.k, *gP = is_dq ? p.dout : p.v;
-      const uint8_t *gX = is_dq ? p.k : p.q, *gY = is_dq ? p.v : p.dout;
-      const uint32_t offX = sbase + (is_dq ? C::kOffK2 : C::kOffX);
-      const uint32_t offY = sbase + (is_dq ? C::kOffV1 : C::kOffY);
-      int xs = 0, ys = 0, xp = 1, yp = 1;  // ring stages, parities of their empty barriers
-      load(mO, gO, sbase, bar_own, t0, pol_own);
+      const bool first = warp == 8;
+      const CUtensorMap *mO = first ? (is_dq ? &tmQ : &tmK) : (is_dq ? &tmDO : &tmV);    // own
+      const CUtensorMap *mR = first ? (is_dq ? &tmK : &tmQ) : (is_dq ? &tmV : &tmDO);    // ring
+      const uint8_t *gO = first ? (is_dq ? p.q : p.k) : (is_dq ? p.dout : p.v);
+      const uint8_t *gR = first ? (is_dq ? p.k : p.q) : (is_dq ? p.v : p.dout);
+      const uint32_t ring = sbase + (first ? (is_dq ? C::kOffK2 : C::kOffX)
+                                           : (is_dq ? C::kOffV1 : C::kOffY));
+      const uint32_t own = first ? 0 : 1;
+      const uint32_t bar_full = first ? bar_x_full : bar_y_full;
+      const uint32_t bar_empty = first ? bar_x_empty : bar_y_empty;
+      int rs = 0, rp = 1;  // ring stage, parity of its empty barrier
+      load(mO, gO, sbase + own * C::kTileBytes, bar_own + 8 * own, t0, pol_own);
       n_own = 1;
       for (int j = 0; j < T && ok; ++j) {
-        ok = wait(bar_x_empty + 8 * xs, xp);
+        ok = wait(bar_empty + 8 * rs, rp);
         if (!ok) break;
-        load(mX, gX, offX + xs * C::kTileBytes, bar_x_full + 8 * xs, j * 128, pol_ring);
-        ++n_x;
-        if (++xs == nx) xs = 0, xp ^= 1;
-        if (!is_dq) {
-          ok = wait(bar_stat_empty + 8 * (j & 1), ((j >> 1) & 1) ^ 1);
+        load(mR, gR, ring + rs * C::kTileBytes, bar_full + 8 * rs, j * 128, pol_ring);
+        ++n_ring;
+        if (++rs == stages) rs = 0, rp ^= 1;
+        if (!is_dq && first) {
+          const int s = j & 1;
+          ok = wait(bar_stat_empty + 8 * s, ((j >> 1) & 1) ^ 1);
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(bar_stat + 8 * (j & 1), 1024);
-            bulk_load(sbase + C::kOffStat + (j & 1) * 1024,
-                      p.stat + (static_cast<int64_t>(bh) * T + j) * 256, 1024, bar_stat + 8 * (j & 1));
+            mbar_arrive_expect_tx(bar_stat + 8 * s, 1024);
+            bulk_load(sbase + C::kOffStat + s * 1024,
+                      p.stat + (static_cast<int64_t>(bh) * T + j) * 256, 1024, bar_stat + 8 * s);
           }
           __syncwarp();
           ++n_stat;
         }
-        if (j == 0) {
-          load(mP, gP, sbase + C::kTileBytes, bar_own + 8, t0, pol_own);
-          n_own = 2;
-        }
-        ok = wait(bar_y_empty + 8 * ys, yp);
-        if (!ok) break;
-        load(mY, gY, offY + ys * C::kTileBytes, bar_y_full + 8 * ys, j * 128, pol_ring);
-        ++n_y;
-        if (++ys == ny) ys = 0, yp ^= 1;
         if (j == 0 && nt == 2) {
-          load(mO, gO, sbase + 2 * C::kTileBytes, bar_own + 16, t0 + 128, pol_own);
-          load(mP, gP, sbase + 3 * C::kTileBytes, bar_own + 24, t0 + 128, pol_own);
-          n_own = 4;
+          load(mO, gO, sbase + (2 + own) * C::kTileBytes, bar_own + 8 * (2 + own), t0 + 128, pol_own);
+          n_own = 2;
         }
       }
     } else if (warp == 9) {
@@ -671,7 +692,7 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int tok = is_dq ? t0 + 128 * h + row : t0 + row;
       const float f = !is_dq && h == 0 ? 1.0f : p.scale;
       __nv_bfloat16 *base = is_dq ? p.dq : h == 0 ? p.dv : p.dk;
-      const bool valid = tok < p.N;
+      const bool valid = tok < p.N && (!is_dq || h < nt);
       __nv_bfloat16 *dst = base + bwd_row(p, bh, valid ? tok : 0, D);
       const uint32_t tA = tmem + lane_bits + (h == 0 ? C::kColA0 : C::kColA1);
 #pragma unroll
@@ -705,12 +726,12 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (*abort_flag) {
     // asynchronous work lands before shared and tensor memory are released:
     // of every stage the last load issued into it
-    if (warp == 8 && lane == 0) {
-      for (int i = 0; i < n_own; ++i) mbar_wait_drain(bar_own + 8 * i, 0, kWaitLimitNs);
-      for (int i = max(n_x - nx, 0); i < n_x; ++i)
-        mbar_wait_drain(bar_x_full + 8 * (i % nx), (i / nx) & 1, kWaitLimitNs);
-      for (int i = max(n_y - ny, 0); i < n_y; ++i)
-        mbar_wait_drain(bar_y_full + 8 * (i % ny), (i / ny) & 1, kWaitLimitNs);
+    if ((warp == 8 || warp == 10) && lane == 0) {
+      const uint32_t own = warp == 8 ? 0 : 1, bar_full = warp == 8 ? bar_x_full : bar_y_full;
+      for (int i = 0; i < n_own; ++i)
+        mbar_wait_drain(bar_own + 8 * (2 * i + own), 0, kWaitLimitNs);
+      for (int i = max(n_ring - stages, 0); i < n_ring; ++i)
+        mbar_wait_drain(bar_full + 8 * (i % stages), (i / stages) & 1, kWaitLimitNs);
       for (int i = max(n_stat - 2, 0); i < n_stat; ++i)
         mbar_wait_drain(bar_stat + 8 * (i & 1), (i >> 1) & 1, kWaitLimitNs);
     }

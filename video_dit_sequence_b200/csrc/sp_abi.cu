@@ -889,7 +889,8 @@ sp_status launch_attention_backward(const CUtensorMap *m, const sp::AttnBwdParam
   sp::attention_delta_kernel<D><<<tiles + pad, 256, 0, cs>>>(p);
   sp_status st = launch_status(cudaGetLastError());
   if (st != SP_OK) return st;
-  const unsigned ctas = static_cast<unsigned>(p.BH) * (p.T + (p.T + 1) / 2);
+  const unsigned ctas =
+      static_cast<unsigned>(p.BH) * (p.T + (p.T + p.dq_tiles - 1) / p.dq_tiles);
   sp::attention_backward_kernel<D><<<ctas, C::kThreads, C::kSmemBytes, cs>>>(m[0], m[1], m[2], m[3],
                                                                              p);
   return launch_status(cudaGetLastError());
@@ -933,6 +934,10 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
   p.hsplit = Hx;
   p.T = (N + 127) / 128;
   p.BH = B * H;
+  // dQ CTAs of one query tile while all CTAs fit the 148 SMs at once (1,024
+  // tokens x 4 heads of 64: TODO instead of TODO us); of two otherwise, which halves
+  // their loads.
+  p.dq_tiles = static_cast<int64_t>(p.BH) * 2 * p.T <= 148 ? 1 : 2;
   p.nl_split = rank_major ? Nl : 0;
   p.scale = s->scale > 0.f ? s->scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.scale_log2e = p.scale * 1.4426950408889634f;
