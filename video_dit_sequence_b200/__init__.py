@@ -20,8 +20,10 @@ Layouts (bf16, contiguous):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 from typing import Optional
@@ -221,15 +223,25 @@ def launch_count() -> int:
 
 # ---------------------------------------------------------------- tensors
 
-def _torch():
-    import torch
-    return torch
+_torch_module = None
 
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+# The helpers below run on every call, which for a short sequence takes the
+# GPU a few microseconds: they avoid the torch.cuda wrappers' Python.
 
 def _ptr(t, shape, name, dtype=None):
-    torch = _torch()
+    """Address of a checked tensor (None stays None)."""
     if t is None:
         return None
+    torch = _torch()
     dtype = dtype or torch.bfloat16
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -237,18 +249,19 @@ def _ptr(t, shape, name, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if tuple(t.shape) != tuple(shape) and t.numel() != math.prod(shape):
+    if t.shape != shape and t.numel() != math.prod(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream, device):
-    torch = _torch()
+    """Handle of the stream a call runs on: the given one, else the device's
+    current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, tensors on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _resolve_device(stream, device):
@@ -259,17 +272,25 @@ def _resolve_device(stream, device):
     return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _same_device(*tensors):
     """All operands must live on one CUDA device; the call runs with that
     device current (the library resolves its per-device state from it)."""
     torch = _torch()
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"operands on several devices: {sorted(map(str, devs))}")
-    dev = devs.pop()
+    dev = None
+    for t in tensors:
+        if t is not None and t.device != dev:
+            if dev is not None:
+                devs = {t.device for t in tensors if t is not None}
+                raise ValueError(f"operands on several devices: {sorted(map(str, devs))}")
+            dev = t.device
+    if dev is None:
+        raise ValueError("operands on several devices: []")
     if dev.type != "cuda":
         raise TypeError("operands must be CUDA tensors")
-    return torch.cuda.device(dev)
+    return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _check(status: int, where: str):
@@ -515,6 +536,7 @@ def out_projection(o, w, bias, y, shape: Shape, layout: str = "seq", stream=None
             O_LAYOUTS[layout], ctypes.byref(s), _stream(stream, o.device)), "sp_out_projection")
 
 
+@functools.lru_cache(maxsize=256)
 def attention_backward_workspace(shape: Shape) -> int:
     """Bytes of the workspace of attention_backward and
     attention_backward_seqsharded."""
@@ -539,7 +561,7 @@ def _attention_backward(name, ts, q, k, v, o, lse, do, dq, dk, dv, shape, worksp
             _ptr(q, ts, "q"), _ptr(k, ts, "k"), _ptr(v, ts, "v"), _ptr(o, ts, "o"),
             _ptr(lse, shape.lse_shape, "lse", torch.float32), _ptr(do, ts, "do"),
             _ptr(dq, ts, "dq"), _ptr(dk, ts, "dk"), _ptr(dv, ts, "dv"),
-            ctypes.c_void_p(ws.data_ptr()), ctypes.byref(s), st), name)
+            ws.data_ptr(), ctypes.byref(s), st), name)
 
 
 def attention_backward(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None, stream=None):
@@ -622,6 +644,7 @@ def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: floa
             "sp_layer_norm")
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_backward_workspace(shape: Shape, hidden: int) -> int:
     """Bytes of layer_norm_backward's workspace."""
     s = shape.c()
@@ -654,7 +677,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=Non
             _ptr(weight, pshape, "weight", dtype), _ptr(mean, rows, "mean", torch.float32),
             _ptr(rstd, rows, "rstd", torch.float32), _ptr(dx, rows + (hidden,), "dx"),
             _ptr(dweight, pshape, "dweight", dtype), _ptr(dbias, pshape, "dbias", dtype),
-            None if ws is None else ctypes.c_void_p(ws.data_ptr()), hidden, layout, ptype,
+            None if ws is None else ws.data_ptr(), hidden, layout, ptype,
             ctypes.byref(s), st), "sp_layer_norm_backward")
 
 
@@ -720,7 +743,7 @@ def attention_ulysses_peer(q_shards, k_group, v_group, o_shards, shape: Shape, r
     local = [x for x in (*q_shards, *o_shards) if not isinstance(x, int)]
 
     def addr(x, name):
-        return x if isinstance(x, int) else _ptr(x, shape.rank_shard, name).value
+        return x if isinstance(x, int) else _ptr(x, shape.rank_shard, name)
 
     qa = (ctypes.c_void_p * P)(*[addr(x, f"q_shards[{r}]") for r, x in enumerate(q_shards)])
     oa = (ctypes.c_void_p * P)(*[addr(x, f"o_shards[{r}]") for r, x in enumerate(o_shards)])
@@ -755,7 +778,7 @@ def _addr_array(xs, shape_, name):
             if not isinstance(x, _torch().Tensor) or not x.is_cuda:
                 raise TypeError(f"{name}[{i}] must be a CUDA tensor or an address")
             return x.data_ptr()
-        return _ptr(x, shape_, f"{name}[{i}]").value
+        return _ptr(x, shape_, f"{name}[{i}]")
     return (ctypes.c_void_p * len(xs))(*[addr(x, i) for i, x in enumerate(xs)])
 
 
