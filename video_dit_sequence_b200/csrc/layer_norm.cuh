@@ -12,11 +12,22 @@
 // every output is rounded once.
 //
 // Both passes are bound by memory: the forward moves 4 bytes an element, the
-// backward 6.  So each element is read once and kept in registers as it came
-// (packed bf16) for the statistics and the result.
+// backward 6.  At the rate of the memory an SM has 22 (33) instructions for an
+// element, so what is done once per thread and row must be spread over many
+// elements: a team of warps takes a row, each thread V vectors of 8 columns (up
+// to 6 forward, 3 backward, where both gradient sums of every column stay in
+// registers).  One vector a thread and a block a row was bound by instructions:
+// 547 us forward and 644 us backward at 75,600 x 5,120, against TODO and TODO.
+// The parameters lie in shared memory in fp32.  Each thread copies its own
+// columns of the next three rows into shared memory (cp.async, which needs no
+// synchronisation), so that some 100 KB an SM are in flight.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
+
+#include "attention_backward.cuh"
+#include "permute.cuh"
+#include "sm100.cuh"
 
 namespace sp {
 
@@ -33,18 +44,32 @@ struct LnParams {
   void *dweight, *dbias;   // backward, or null
   int32_t C8;              // C / 8
   int32_t P, B, Nl, N;
-  int64_t rows;            // P * B * Nl
+  FastDiv div_n, div_nl;
   int32_t per_sample;      // w and b are [B][C]
   int32_t param_f32;       // fp32 parameters (and their gradients), else bf16
   float eps, inv_c;
 };
 
-// The input rows are read once: past L1, so that the parameters stay there.
-__device__ __forceinline__ uint4 ln_load(const uint4 *p) {
+constexpr int kLnFwdVec = 6, kLnBwdVec = 3;  // vectors of a thread at most
+constexpr int kLnStages = 4;                 // rows of a team's ring
+constexpr int kLnMaxWarps = 16;              // of a block
+// Blocks an SM holds (by registers: 128 a thread, or 64 with few vectors).
+__host__ __device__ constexpr int ln_blocks_per_sm(int V, bool backward) {
+  return !backward && V <= 2 ? 2 : 1;
+}
+
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "r"(addr));
   return v;
 }
 
@@ -85,239 +110,361 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-constexpr int kLnFwdWarps = 4;
+// Rows of one group of a pass, in the order of the logical sequence (so that
+// sums do not depend on P): i-th valid row of all samples, or of sample `g`
+// when every sample has its own parameters.
+__device__ __forceinline__ int64_t ln_row(const LnParams &p, uint32_t g, uint32_t i) {
+  const uint32_t b = p.per_sample ? g : fdiv(i, p.div_n);
+  const uint32_t t = p.per_sample ? i : i - b * static_cast<uint32_t>(p.N);
+  const uint32_t r = fdiv(t, p.div_nl);
+  return static_cast<int64_t>(r * p.B + b) * p.Nl + (t - r * p.Nl);
+}
 
-// One warp per row; lane l holds vectors l, l + 32, ... (V of them at most)
-// of 8 elements.  The variance is summed around the mean in a second sweep
-// over the registers, so that a large mean costs no digits.
-template <int V>
-__global__ void __launch_bounds__(32 * kLnFwdWarps) layer_norm_kernel(const LnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kLnFwdWarps + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int64_t slot = row / p.Nl;
-  const int n = static_cast<int>(row - slot * p.Nl);
-  const int r = static_cast<int>(slot / p.B), b = static_cast<int>(slot - static_cast<int64_t>(r) * p.B);
-  uint4 *y = p.y + row * p.C8;
-  if (static_cast<int64_t>(r) * p.Nl + n >= p.N) {  // padding: zeros, and statistics of 0
-    for (int c = lane; c < p.C8; c += 32) y[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 0) {
-      if (p.mean != nullptr) p.mean[row] = 0.f;
-      if (p.rstd != nullptr) p.rstd[row] = 0.f;
-    }
-    return;
+// Sums of M values over a team of W warps (its warps' slots of `red`, which the
+// team's previous sums do not use), in warp order; every thread gets them.
+template <int M>
+__device__ __forceinline__ void team_sums(float (&v)[M], float (*red)[kLnMaxWarps], int team, int W) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = warp_sum(v[m]);
+  if (W == 1) return;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) red[m][threadIdx.x >> 5] = v[m];
   }
-  const uint4 *x = p.x + row * p.C8;
-  uint4 v[V];
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * W) : "memory");
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = lane + 32 * i;
-    v[i] = c < p.C8 ? ln_load(x + c) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float f[8];
-    ln_unpack(v[i], f);
-    s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-  }
-  const float mean = warp_sum(s) * p.inv_c;
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (lane + 32 * i < p.C8) {
-      float f[8];
-      ln_unpack(v[i], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = f[e] - mean;
-        q = fmaf(d, d, q);
-      }
-    }
-  }
-  const float rstd = 1.0f / sqrtf(warp_sum(q) * p.inv_c + p.eps);
-  if (lane == 0) {
-    if (p.mean != nullptr) p.mean[row] = mean;
-    if (p.rstd != nullptr) p.rstd[row] = rstd;
-  }
-  const int64_t prow = p.per_sample ? b : 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = lane + 32 * i;
-    if (c < p.C8) {
-      float f[8], t[8];
-      ln_unpack(v[i], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = (f[e] - mean) * rstd;
-      if (p.weight != nullptr) {
-        ln_param8(p.weight, p.param_f32, prow, p.C8, c, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= t[e];
-      }
-      if (p.bias != nullptr) {
-        ln_param8(p.bias, p.param_f32, prow, p.C8, c, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] += t[e];
-      }
-      y[c] = ln_pack(f);
-    }
+  for (int m = 0; m < M; ++m) {
+    float t = 0.f;
+    for (int k = team * W; k < (team + 1) * W; ++k) t += red[m][k];
+    v[m] = t;
   }
 }
 
-// Rows of one group of the backward pass, in the order of the logical
-// sequence (so that sums do not depend on P): i-th valid row of all samples,
-// or of sample `g` when every sample has its own parameters.
-__device__ __forceinline__ int64_t ln_row(const LnParams &p, int g, int64_t i) {
-  int b = g;
-  int t;
-  if (p.per_sample) {
-    t = static_cast<int>(i);
-  } else {
-    b = static_cast<int>(i / p.N);
-    t = static_cast<int>(i - static_cast<int64_t>(b) * p.N);
+// Parameter row `row` into shared memory in fp32; `none` where there is none.
+__device__ __forceinline__ void ln_stage_params(const LnParams &p, const void *src, float none,
+                                                int64_t row, float4 *dst) {
+  for (int c = threadIdx.x; c < p.C8; c += blockDim.x) {
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = none;
+    if (src != nullptr) ln_param8(src, p.param_f32, row, p.C8, c, t);
+    // the halves of a vector apart, so that consecutive lanes read
+    // consecutive 16-byte words
+    dst[c] = make_float4(t[0], t[1], t[2], t[3]);
+    dst[p.C8 + c] = make_float4(t[4], t[5], t[6], t[7]);
   }
-  const int r = t / p.Nl;
-  return (static_cast<int64_t>(r) * p.B + b) * p.Nl + (t - r * p.Nl);
 }
 
-// Backward: a block takes rows blockIdx.x, blockIdx.x + gridDim.x, ... of
-// group blockIdx.y; thread t holds V vectors of 8 columns (t, t + blockDim.x)
-// of every row, with their weights and their two gradient sums in registers,
-// so that the rows are read once for dx and for the parameters' gradients.
-// The sums leave as one partial row per block, which layer_norm_grad_kernel
-// adds in block order: the result depends on no race.
-template <int V, bool kGrad>
-__global__ void __launch_bounds__(512) layer_norm_backward_kernel(const LnParams p) {
-  __shared__ float2 red[2][16];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nwarps = blockDim.x >> 5;
-  const int g = blockIdx.y;
-  const int64_t nrows = p.per_sample ? p.N : static_cast<int64_t>(p.B) * p.N;
-  float w[V][8], dw[V][8], db[V][8];
+// Columns as four pairs of fp32.
+__device__ __forceinline__ void ln_unpack2(const uint4 &v, uint64_t *f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = tid + v * blockDim.x;
+  for (int i = 0; i < 4; ++i) f[i] = f2_pack_bits(w[i] << 16, w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 ln_pack2(const uint64_t *f) {
+  uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[v][e] = 1.f, dw[v][e] = 0.f, db[v][e] = 0.f;
-    if (p.weight != nullptr && c < p.C8)
-      ln_param8(p.weight, p.param_f32, p.per_sample ? g : 0, p.C8, c, w[v]);
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f[i], lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
   }
-  uint4 xv[V], dv[V];
-  float mean = 0.f, rstd = 0.f;
-  auto load = [&](int64_t row) {
-    const uint4 *x = p.x + row * p.C8, *dy = p.dy + row * p.C8;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = tid + v * blockDim.x;
-      xv[v] = c < p.C8 ? ln_load(x + c) : make_uint4(0u, 0u, 0u, 0u);
-      dv[v] = c < p.C8 ? ln_load(dy + c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    mean = __ldg(p.mean_in + row);
-    rstd = __ldg(p.rstd_in + row);
-  };
-  int64_t i = blockIdx.x;
-  int64_t row = 0;
-  if (i < nrows) load(row = ln_row(p, g, i));
-  for (int ph = 0; i < nrows; i += gridDim.x, ph ^= 1) {
-    float gv[V][8], xh[V][8];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float d[8];
-      ln_unpack(xv[v], xh[v]);
-      ln_unpack(dv[v], d);
-      const bool in = tid + v * static_cast<int>(blockDim.x) < p.C8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[v][e] = in ? (xh[v][e] - mean) * rstd : 0.f;
-        if (kGrad) {
-          dw[v][e] = fmaf(d[e], xh[v][e], dw[v][e]);
-          db[v][e] += d[e];
-        }
-        gv[v][e] = d[e] * w[v][e];
-        s1 += gv[v][e];
-        s2 = fmaf(gv[v][e], xh[v][e], s2);
-      }
-    }
-    const float rs = rstd;
-    uint4 *dx = p.y + row * p.C8;
-    // the next row's loads are in flight across the reduction
-    if (i + gridDim.x < nrows) load(row = ln_row(p, g, i + gridDim.x));
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (lane == 0) red[ph][warp] = make_float2(s1, s2);
-    __syncthreads();  // one barrier a row: the next row uses the other half of red
-    s1 = 0.f;
-    s2 = 0.f;
-    for (int k = 0; k < nwarps; ++k) {
-      const float2 t = red[ph][k];
-      s1 += t.x;
-      s2 += t.y;
-    }
-    s1 *= p.inv_c;
-    s2 *= p.inv_c;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = tid + v * blockDim.x;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = rs * (gv[v][e] - s1 - xh[v][e] * s2);
-      if (c < p.C8) dx[c] = ln_pack(f);
-    }
-  }
-  if (kGrad) {
-    float4 *out = reinterpret_cast<float4 *>(
-        p.partial + (static_cast<int64_t>(g) * gridDim.x + blockIdx.x) * 16 * p.C8);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = tid + v * blockDim.x;
-      if (c < p.C8) {
-        out[2 * c] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-        out[2 * c + 1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
-        out[2 * (p.C8 + c)] = make_float4(db[v][0], db[v][1], db[v][2], db[v][3]);
-        out[2 * (p.C8 + c) + 1] = make_float4(db[v][4], db[v][5], db[v][6], db[v][7]);
-      }
-    }
-  }
-  // padding rows of dx are zero (all samples', shared among all blocks)
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void ln_load_params(const float4 *src, int C8, int c, uint64_t *f) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(src)[c];
+  const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(src)[C8 + c];
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
+}
+
+// Zeroes rows past N of y (and of the statistics), shared among all blocks.
+__device__ __forceinline__ void ln_zero_padding(const LnParams &p, bool stats) {
   const int64_t pad = static_cast<int64_t>(p.P) * p.Nl - p.N;
   const int64_t nblk = static_cast<int64_t>(gridDim.x) * gridDim.y;
-  for (int64_t j = static_cast<int64_t>(g) * gridDim.x + blockIdx.x; j < pad * p.B; j += nblk) {
+  for (int64_t j = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; j < pad * p.B;
+       j += nblk) {
     const int b = static_cast<int>(j / pad);
     const int t = static_cast<int>(p.N + (j - b * pad));
     const int r = t / p.Nl;
-    uint4 *dx = p.y + ((static_cast<int64_t>(r) * p.B + b) * p.Nl + (t - r * p.Nl)) * p.C8;
-    for (int c = tid; c < p.C8; c += blockDim.x) dx[c] = make_uint4(0u, 0u, 0u, 0u);
+    const int64_t row = (static_cast<int64_t>(r) * p.B + b) * p.Nl + (t - r * p.Nl);
+    for (int c = threadIdx.x; c < p.C8; c += blockDim.x)
+      p.y[row * p.C8 + c] = make_uint4(0u, 0u, 0u, 0u);
+    if (stats && threadIdx.x == 0) {
+      if (p.mean != nullptr) p.mean[row] = 0.f;
+      if (p.rstd != nullptr) p.rstd[row] = 0.f;
+    }
   }
 }
 
-constexpr int kLnGradCols = 32, kLnGradRows = 16;
+// Forward.  The variance is summed around the mean in a second sweep over the
+// registers, so that a large mean costs no digits.  Team i takes rows i,
+// i + teams, ... of group blockIdx.y.
+template <int V>
+__global__ void __launch_bounds__(32 * kLnMaxWarps, ln_blocks_per_sm(V, false))
+layer_norm_kernel(const LnParams p, int W) {
+  constexpr int K = kLnStages;
+  __shared__ float red[4][kLnMaxWarps];
+  extern __shared__ __align__(16) uint8_t ln_smem[];
+  float4 *const sw = reinterpret_cast<float4 *>(ln_smem), *const sb = sw + 2 * p.C8;
+  const int team = (threadIdx.x >> 5) / W, tn = 32 * W, tt = threadIdx.x - team * tn;
+  const uint32_t g = blockIdx.y;
+  const uint32_t nrows = p.per_sample ? p.N : p.B * p.N;  // below 2^31
+  const uint32_t block_teams = blockDim.x / tn, teams = gridDim.x * block_teams;
+  const uint32_t ring = smem_u32(sb + 2 * p.C8) + threadIdx.x * 16;
+  const uint32_t vec = blockDim.x * 16, line = V * vec;  // bytes between vectors, rows
+  auto fetch = [&](int s, uint32_t i) {
+    if (i < nrows) {
+      const uint4 *x = p.x + ln_row(p, g, i) * p.C8;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (tt + v * tn < p.C8) cp_async16(ring + s * line + v * vec, x + tt + v * tn, 16);
+    }
+    cp_async_commit();
+  };
+  uint32_t i = blockIdx.x * block_teams + team;
+#pragma unroll
+  for (int s = 0; s < K - 1; ++s) fetch(s, i + s * teams);
+  ln_stage_params(p, p.weight, 1.f, p.per_sample ? g : 0, sw);
+  ln_stage_params(p, p.bias, 0.f, p.per_sample ? g : 0, sb);
+  __syncthreads();
+  int s = 0, ph = 0;
+  for (; i < nrows; i += teams, ph ^= 2) {
+    cp_async_wait_group<K - 2>();
+    uint64_t f[V][4];
+    uint64_t acc = f2_pack(0.f, 0.f), acc2 = acc;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      ln_unpack2(tt + v * tn < p.C8 ? ld_shared_v4(ring + s * line + v * vec)
+                                    : make_uint4(0u, 0u, 0u, 0u), f[v]);
+      acc = f2_add(acc, f2_add(f[v][0], f[v][1]));
+      acc2 = f2_add(acc2, f2_add(f[v][2], f[v][3]));
+    }
+    // the stage read in the last step takes the row K - 1 steps ahead
+    fetch(s == 0 ? K - 1 : s - 1, i + (K - 1) * teams);
+    s = s + 1 == K ? 0 : s + 1;
+    float sum[1] = {f2_sum(f2_add(acc, acc2))};
+    team_sums<1>(sum, red + ph, team, W);
+    const float mean = sum[0] * p.inv_c;
+    const uint64_t nmean2 = f2_pack(-mean, -mean);
+    acc = acc2 = f2_pack(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[v][e] = f2_add(f[v][e], nmean2);
+      if (tt + v * tn < p.C8) {
+        acc = f2_fma(f[v][0], f[v][0], f2_fma(f[v][1], f[v][1], acc));
+        acc2 = f2_fma(f[v][2], f[v][2], f2_fma(f[v][3], f[v][3], acc2));
+      }
+    }
+    sum[0] = f2_sum(f2_add(acc, acc2));
+    team_sums<1>(sum, red + ph + 1, team, W);
+    const float rstd = 1.0f / sqrtf(sum[0] * p.inv_c + p.eps);
+    const uint64_t rstd2 = f2_pack(rstd, rstd);
+    const int64_t row = ln_row(p, g, i);
+    if (tt == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tt + v * tn;
+      if (c < p.C8) {
+        uint64_t w[4], b[4];
+        ln_load_params(sw, p.C8, c, w);
+        ln_load_params(sb, p.C8, c, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[v][e] = f2_fma(f2_mul(f[v][e], rstd2), w[e], b[e]);
+        p.y[row * p.C8 + c] = ln_pack2(f[v]);
+      }
+    }
+  }
+  ln_zero_padding(p, true);
+}
 
-// Sums the blocks' partial rows [groups][blocks][2][C] in block order: thread
-// (x, y) adds column x of partial rows y, y + 16, ..., then the 16 sums of a
-// column are added in order.  blockIdx.y is the group, blockIdx.z 0 for dw, 1 for db.
-__global__ void __launch_bounds__(kLnGradCols *kLnGradRows)
-layer_norm_grad_kernel(const LnParams p, int blocks) {
-  __shared__ float red[kLnGradRows][kLnGradCols + 1];
-  const int x = threadIdx.x % kLnGradCols, y = threadIdx.x / kLnGradCols;
-  const int64_t C = 8ll * p.C8;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * kLnGradCols + x;
+// Backward.  Each team keeps the gradient sums of its rows; a block's teams are
+// added in order, and the sums leave as one partial row per block, which
+// layer_norm_grad_kernel adds in block order: the result depends on no race.
+// Between the sums over a row and its result the row stays packed.
+template <int V, bool kGrad>
+__global__ void __launch_bounds__(32 * kLnMaxWarps, ln_blocks_per_sm(V, true))
+layer_norm_backward_kernel(const LnParams p, int W) {
+  constexpr int K = kLnStages;
+  __shared__ float red[4][kLnMaxWarps];
+  extern __shared__ __align__(16) uint8_t ln_smem[];
+  // (the kernel that adds the partial rows may take its place meanwhile)
+  asm volatile("griddepcontrol.launch_dependents;");
+  float4 *const sw = reinterpret_cast<float4 *>(ln_smem);
+  const int team = (threadIdx.x >> 5) / W, tn = 32 * W, tt = threadIdx.x - team * tn;
+  const uint32_t g = blockIdx.y;
+  const uint32_t nrows = p.per_sample ? p.N : p.B * p.N;  // below 2^31
+  const uint32_t block_teams = blockDim.x / tn, teams = gridDim.x * block_teams;
+  const uint32_t ring = smem_u32(sw + 2 * p.C8) + threadIdx.x * 16;
+  const uint32_t vec = blockDim.x * 16, line = 2 * V * vec;
+  auto fetch = [&](int s, uint32_t i) {
+    if (i < nrows) {
+      const int64_t off = ln_row(p, g, i) * p.C8;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = tt + v * tn;
+        if (c < p.C8) {
+          cp_async16(ring + s * line + 2 * v * vec, p.x + off + c, 16);
+          cp_async16(ring + s * line + (2 * v + 1) * vec, p.dy + off + c, 16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  uint32_t i = blockIdx.x * block_teams + team;
+#pragma unroll
+  for (int s = 0; s < K - 1; ++s) fetch(s, i + s * teams);
+  int64_t row = 0;
+  float next_mean = 0.f, next_rstd = 0.f;
+  auto stats = [&](uint32_t j) {
+    if (j < nrows) {
+      row = ln_row(p, g, j);
+      next_mean = __ldg(p.mean_in + row);
+      next_rstd = __ldg(p.rstd_in + row);
+    }
+  };
+  stats(i);
+  ln_stage_params(p, p.weight, 1.f, p.per_sample ? g : 0, sw);
+  __syncthreads();
+  const uint64_t zero2 = f2_pack(0.f, 0.f);
+  uint64_t dw[V][4], db[V][4];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dw[v][e] = db[v][e] = zero2;
+  int s = 0, ph = 0;
+  for (; i < nrows; i += teams, ph ^= 2) {
+    cp_async_wait_group<K - 2>();
+    const uint64_t nmean2 = f2_pack(-next_mean, -next_mean), rstd2 = f2_pack(next_rstd, next_rstd);
+    uint4 *dx = p.y + row * p.C8;
+    uint4 xp[V], dp[V];
+    uint64_t a1 = zero2, a2 = zero2;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tt + v * tn;
+      const bool in = c < p.C8;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      xp[v] = in ? ld_shared_v4(ring + s * line + 2 * v * vec) : zero;
+      dp[v] = in ? ld_shared_v4(ring + s * line + (2 * v + 1) * vec) : zero;
+      uint64_t x[4], d[4], w[4];
+      ln_unpack2(xp[v], x);
+      ln_unpack2(dp[v], d);
+      ln_load_params(sw, p.C8, in ? c : 0, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t xh = f2_mul(f2_add(x[e], nmean2), rstd2);
+        const uint64_t gv = f2_mul(d[e], w[e]);   // (0 past the row)
+        a1 = f2_add(a1, gv);
+        a2 = f2_fma(gv, xh, a2);
+        if (kGrad) {
+          dw[v][e] = f2_fma(d[e], xh, dw[v][e]);
+          db[v][e] = f2_add(db[v][e], d[e]);
+        }
+      }
+    }
+    fetch(s == 0 ? K - 1 : s - 1, i + (K - 1) * teams);
+    s = s + 1 == K ? 0 : s + 1;
+    stats(i + teams);  // in flight across the reduction
+    float sums[2] = {f2_sum(a1), f2_sum(a2)};
+    team_sums<2>(sums, red + ph, team, W);
+    const float s1 = -sums[0] * p.inv_c, s2 = -sums[1] * p.inv_c;
+    const uint64_t ns1 = f2_pack(s1, s1), ns2 = f2_pack(s2, s2);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = tt + v * tn;
+      if (c < p.C8) {
+        uint64_t x[4], d[4], w[4];
+        ln_unpack2(xp[v], x);
+        ln_unpack2(dp[v], d);
+        ln_load_params(sw, p.C8, c, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t xh = f2_mul(f2_add(x[e], nmean2), rstd2);
+          x[e] = f2_mul(f2_fma(xh, ns2, f2_fma(d[e], w[e], ns1)), rstd2);
+        }
+        dx[c] = ln_pack2(x);
+      }
+    }
+  }
+  if (kGrad) {
+    // the block's teams in order, through the ring: [dw, db][half][C8] float4
+    cp_async_wait_group<0>();
+    ulonglong2 *acc = reinterpret_cast<ulonglong2 *>(sw + 2 * p.C8);
+    for (uint32_t k = 0; k < block_teams; ++k) {
+      __syncthreads();
+      if (static_cast<uint32_t>(team) != k) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = tt + v * tn;
+        if (c >= p.C8) continue;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint64_t *a = (h < 2 ? dw[v] : db[v]) + 2 * (h & 1);
+          ulonglong2 t = make_ulonglong2(a[0], a[1]);
+          ulonglong2 *slot = acc + h * p.C8 + c;
+          if (k > 0) {
+            const ulonglong2 o = *slot;
+            t = make_ulonglong2(f2_add(o.x, t.x), f2_add(o.y, t.y));
+          }
+          *slot = t;
+        }
+      }
+    }
+    __syncthreads();
+    float4 *out = reinterpret_cast<float4 *>(p.partial) +
+                  (static_cast<int64_t>(g) * gridDim.x + blockIdx.x) * 4 * p.C8;
+    const float4 *sums = sw + 2 * p.C8;
+    for (int c = threadIdx.x; c < p.C8; c += blockDim.x)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) out[(h >> 1) * 2 * p.C8 + 2 * c + (h & 1)] = sums[h * p.C8 + c];
+  }
+  ln_zero_padding(p, false);
+}
+
+// Sums the blocks' partial rows [groups][blocks][2][C] in a fixed order: thread
+// (x, y) adds columns 4x .. 4x + 3 of partial rows y, y + 32, ..., then the 32
+// sums of a column are added in order.  blockIdx.y is the group, blockIdx.z 0
+// for dw, 1 for db; 8 x 32 threads.
+constexpr int kLnGradRows = 32;
+__global__ void __launch_bounds__(256) layer_norm_grad_kernel(const LnParams p, int blocks) {
+  __shared__ float4 red[kLnGradRows][8];
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int64_t C4 = 2ll * p.C8;  // float4 of a row
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 8 + x;
   const int64_t g = blockIdx.y;
   const int which = blockIdx.z;
-  float s = 0.f;
-  if (col < C)
-    for (int k = y; k < blocks; k += kLnGradRows)
-      s += p.partial[((g * blocks + k) * 2 + which) * C + col];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (col < C4) {
+    const float4 *src = reinterpret_cast<const float4 *>(p.partial) + (g * blocks * 2 + which) * C4 + col;
+#pragma unroll 8
+    for (int k = y; k < blocks; k += kLnGradRows) {
+      const float4 v = src[static_cast<int64_t>(k) * 2 * C4];
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+  }
   red[y][x] = s;
   __syncthreads();
-  if (y == 0 && col < C) {
+  if (y == 0 && col < C4) {
 #pragma unroll
-    for (int k = 1; k < kLnGradRows; ++k) s += red[k][x];
+    for (int k = 1; k < kLnGradRows; ++k) {
+      const float4 v = red[k][x];
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
     void *out = which ? p.dbias : p.dweight;
     if (p.param_f32)
-      static_cast<float *>(out)[g * C + col] = s;
+      static_cast<float4 *>(out)[g * C4 + col] = s;
     else
-      static_cast<__nv_bfloat16 *>(out)[g * C + col] = __float2bfloat16_rn(s);
+      static_cast<uint2 *>(out)[g * C4 + col] =
+          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 

@@ -753,7 +753,8 @@ sp::LnParams norm_params(const sp_shape *s, int32_t hidden, int32_t param_layout
   p.B = s->B;
   p.N = s->N;
   p.Nl = static_cast<int32_t>((static_cast<int64_t>(s->N) + s->P - 1) / s->P);
-  p.rows = static_cast<int64_t>(p.P) * p.B * p.Nl;
+  p.div_n = sp::make_fastdiv(static_cast<uint32_t>(p.N));
+  p.div_nl = sp::make_fastdiv(static_cast<uint32_t>(p.Nl));
   p.per_sample = param_layout == SP_PARAM_PER_SAMPLE;
   p.param_f32 = param_type == SP_PARAM_FP32;
   p.inv_c = 1.0f / static_cast<float>(hidden);
@@ -761,6 +762,47 @@ sp::LnParams norm_params(const sp_shape *s, int32_t hidden, int32_t param_layout
 }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int kNormMaxSmem = 224 * 1024;
+
+// How a layer norm pass is spread: warps of a team (which takes a row), vectors
+// of a thread, teams of a block.  Blocks of a group: as many as the 148 SMs
+// hold at once; few rows are spread over all SMs.
+struct NormPlan {
+  int W, V, threads, smem, groups;
+  int64_t blocks;  // of a group
+};
+
+NormPlan norm_plan(const sp::LnParams &p, bool backward) {
+  NormPlan pl;
+  const int most = 32 * (backward ? sp::kLnBwdVec : sp::kLnFwdVec);
+  pl.W = (p.C8 + most - 1) / most;
+  pl.V = (p.C8 + 32 * pl.W - 1) / (32 * pl.W);
+  pl.groups = p.per_sample ? p.B : 1;
+  const int64_t nrows = p.per_sample ? p.N : static_cast<int64_t>(p.B) * p.N;
+  const int64_t slots =
+      std::max<int64_t>(1, 148 * sp::ln_blocks_per_sm(pl.V, backward) / pl.groups);
+  const int64_t teams = std::max<int64_t>(
+      1, std::min<int64_t>(sp::kLnMaxWarps / pl.W, (nrows + slots - 1) / slots));
+  pl.blocks = std::min((nrows + teams - 1) / teams, slots);
+  pl.threads = static_cast<int>(teams) * pl.W * 32;
+  // parameters (weight and bias, or weight) and the rings; the backward pass
+  // adds its teams' gradient sums in the rings' place
+  const int params = (backward ? 32 : 64) * p.C8;
+  const int ring = sp::kLnStages * (backward ? 2 : 1) * pl.V * pl.threads * 16;
+  pl.smem = params + std::max(ring, backward ? 64 * p.C8 : 0);
+  return pl;
+}
+
+// Runs launch(integral_constant<int, V>) for V = 1 .. kMax.
+template <int kMax, typename F>
+cudaError_t for_vectors(int V, F launch) {
+  if constexpr (kMax == 0) {
+    return cudaErrorInvalidValue;
+  } else {
+    return V == kMax ? launch(std::integral_constant<int, kMax>()) : for_vectors<kMax - 1>(V, launch);
+  }
+}
 
 sp_status layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
                      float *rstd, int32_t hidden, float eps, int32_t param_layout,
@@ -780,52 +822,54 @@ sp_status layer_norm(const void *x, const void *weight, const void *bias, void *
   p.rstd = rstd;
   p.eps = eps > 0.f ? eps : 1e-6f;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>((p.rows + sp::kLnFwdWarps - 1) / sp::kLnFwdWarps));
-  const dim3 block(32 * sp::kLnFwdWarps);
-  const int v = (p.C8 + 31) / 32;  // vectors per lane
-  if (v <= 1) sp::layer_norm_kernel<1><<<grid, block, 0, cs>>>(p);
-  else if (v <= 2) sp::layer_norm_kernel<2><<<grid, block, 0, cs>>>(p);
-  else if (v <= 4) sp::layer_norm_kernel<4><<<grid, block, 0, cs>>>(p);
-  else if (v <= 6) sp::layer_norm_kernel<6><<<grid, block, 0, cs>>>(p);
-  else if (v <= 8) sp::layer_norm_kernel<8><<<grid, block, 0, cs>>>(p);
-  else if (v <= 12) sp::layer_norm_kernel<12><<<grid, block, 0, cs>>>(p);
-  else if (v <= 16) sp::layer_norm_kernel<16><<<grid, block, 0, cs>>>(p);
-  else if (v <= 20) sp::layer_norm_kernel<20><<<grid, block, 0, cs>>>(p);
-  else sp::layer_norm_kernel<32><<<grid, block, 0, cs>>>(p);
-  static_assert(SP_NORM_MAX_HIDDEN <= 32 * 32 * 8, "a warp holds a row");
-  return launch_status(cudaGetLastError());
-}
-
-// Threads of a block of the backward pass: one vector of 8 columns each up
-// to 1,024 columns, two above.
-int norm_backward_threads(int C8) {
-  const int per = C8 <= 128 ? 1 : 2;
-  return ((C8 + per - 1) / per + 31) / 32 * 32;
-}
-
-// Most blocks of a group of the backward pass: no fewer than eight rows a
-// block, and at most what 148 SMs hold at 1,024 threads and 16 blocks each,
-// over all groups.  Each block leaves one partial row of both gradients.
-int64_t norm_backward_blocks(int64_t nrows, int64_t groups, int C8) {
-  const int threads = norm_backward_threads(C8);
-  const int64_t cap = 148 * std::max(1, std::min(16, 1024 / threads));
-  const int64_t per_group = std::max<int64_t>(1, cap / groups);
-  return std::min<int64_t>((nrows + 7) / 8, per_group);
+  const NormPlan pl = norm_plan(p, false);
+  return launch_status(for_vectors<sp::kLnFwdVec>(pl.V, [&](auto v) {
+    static bool set[kMaxDevices] = {};
+    const auto kernel = sp::layer_norm_kernel<decltype(v)::value>;
+    const cudaError_t e = set_smem_once(kernel, kNormMaxSmem, set);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3(static_cast<unsigned>(pl.blocks), pl.groups), pl.threads, pl.smem, cs>>>(p, pl.W);
+    return cudaGetLastError();
+  }));
 }
 
 int64_t norm_backward_workspace(const sp_shape *s, int32_t hidden) {
   if (check_norm(s, hidden, SP_PARAM_SHARED, SP_PARAM_BF16) != SP_OK) return -1;
-  const int64_t shared = norm_backward_blocks(static_cast<int64_t>(s->B) * s->N, 1, hidden / 8);
-  const int64_t sample = s->B * norm_backward_blocks(s->N, s->B, hidden / 8);
-  return std::max(shared, sample) * 2 * hidden * 4;
+  int64_t rows = 0;
+  for (int32_t layout : {SP_PARAM_SHARED, SP_PARAM_PER_SAMPLE}) {
+    const NormPlan pl = norm_plan(norm_params(s, hidden, layout, SP_PARAM_BF16), true);
+    rows = std::max(rows, pl.blocks * pl.groups);
+  }
+  return rows * 2 * hidden * 4;
 }
 
 template <int V, bool kGrad>
-cudaError_t launch_norm_backward(const sp::LnParams &p, int64_t blocks, int groups, int threads,
-                                 cudaStream_t cs) {
-  sp::layer_norm_backward_kernel<V, kGrad>
-      <<<dim3(static_cast<unsigned>(blocks), groups), threads, 0, cs>>>(p);
+cudaError_t launch_norm_backward(const sp::LnParams &p, const NormPlan &pl, cudaStream_t cs) {
+  static bool set[kMaxDevices] = {};
+  const auto kernel = sp::layer_norm_backward_kernel<V, kGrad>;
+  const cudaError_t e = set_smem_once(kernel, kNormMaxSmem, set);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3(static_cast<unsigned>(pl.blocks), pl.groups), pl.threads, pl.smem, cs>>>(p, pl.W);
   return cudaGetLastError();
+}
+
+// Launches a kernel that may begin before the one in front of it on the stream
+// has ended, and waits for that one itself (griddepcontrol.wait).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, int smem,
+                             cudaStream_t cs, const Args &...args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = cs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 sp_status layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
@@ -853,21 +897,15 @@ sp_status layer_norm_backward(const void *dy, const void *x, const void *weight,
   p.dbias = dbias;
   p.partial = static_cast<float *>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int groups = p.per_sample ? p.B : 1;
-  const int64_t nrows = p.per_sample ? p.N : static_cast<int64_t>(p.B) * p.N;
-  const int64_t blocks = norm_backward_blocks(nrows, groups, p.C8);
-  const int threads = norm_backward_threads(p.C8);
-  const bool one = p.C8 <= threads;
-  const cudaError_t e = one ? (grad ? launch_norm_backward<1, true>(p, blocks, groups, threads, cs)
-                                    : launch_norm_backward<1, false>(p, blocks, groups, threads, cs))
-                            : (grad ? launch_norm_backward<2, true>(p, blocks, groups, threads, cs)
-                                    : launch_norm_backward<2, false>(p, blocks, groups, threads, cs));
-  st = launch_status(e);
+  const NormPlan pl = norm_plan(p, true);
+  st = launch_status(for_vectors<sp::kLnBwdVec>(pl.V, [&](auto v) {
+    return grad ? launch_norm_backward<decltype(v)::value, true>(p, pl, cs)
+                : launch_norm_backward<decltype(v)::value, false>(p, pl, cs);
+  }));
   if (st != SP_OK || !grad) return st;
-  const dim3 grid((hidden + sp::kLnGradCols - 1) / sp::kLnGradCols, groups, 2);
-  sp::layer_norm_grad_kernel<<<grid, sp::kLnGradCols * sp::kLnGradRows, 0, cs>>>(
-      p, static_cast<int>(blocks));
-  return launch_status(cudaGetLastError());
+  const dim3 grid((hidden + 31) / 32, pl.groups, 2);
+  return launch_status(launch_dependent(sp::layer_norm_grad_kernel, grid, dim3(256), 0, cs, p,
+                                        static_cast<int>(pl.blocks)));
 }
 
 // Backward pass of attention (see sp_attention_backward in sp.h).
