@@ -15,7 +15,7 @@
 // backward 6.  At the rate of the memory an SM has 22 (33) instructions for an
 // element, so what is done once per thread and row must be spread over many
 // elements: a team of warps takes a row, each thread V vectors of 8 columns (up
-// to 6 forward, 3 backward, where both gradient sums of every column stay in
+// to 6 forward, 4 backward, where both gradient sums of every column stay in
 // registers).  One vector a thread and a block a row was bound by instructions:
 // 547 us forward and 644 us backward at 75,600 x 5,120, against TODO and TODO.
 // The parameters lie in shared memory in fp32.  Each thread copies its own
@@ -46,16 +46,20 @@ struct LnParams {
   int32_t P, B, Nl, N;
   FastDiv div_n, div_nl;
   int32_t per_sample;      // w and b are [B][C]
+  int32_t linear;          // B or P is 1: row i of the valid ones is row i of memory
   int32_t param_f32;       // fp32 parameters (and their gradients), else bf16
   float eps, inv_c;
 };
 
-constexpr int kLnFwdVec = 6, kLnBwdVec = 3;  // vectors of a thread at most
+constexpr int kLnFwdVec = 6, kLnBwdVec = 4;  // vectors of a thread at most
 constexpr int kLnStages = 4;                 // rows of a team's ring
-constexpr int kLnMaxWarps = 16;              // of a block
-// Blocks an SM holds (by registers: 128 a thread, or 64 with few vectors).
+// Warps of a block at most and blocks of an SM, by registers: 128 a thread (64
+// with few vectors) forward; 80, 128 or, from three vectors on, 168 backward.
+__host__ __device__ constexpr int ln_max_warps(int V, bool backward) {
+  return backward && V != 2 ? 12 : 16;
+}
 __host__ __device__ constexpr int ln_blocks_per_sm(int V, bool backward) {
-  return !backward && V <= 2 ? 2 : 1;
+  return V <= (backward ? 1 : 2) ? 2 : 1;
 }
 
 template <int kPending>
@@ -114,30 +118,39 @@ __device__ __forceinline__ float warp_sum(float v) {
 // sums do not depend on P): i-th valid row of all samples, or of sample `g`
 // when every sample has its own parameters.
 __device__ __forceinline__ int64_t ln_row(const LnParams &p, uint32_t g, uint32_t i) {
+  if (p.linear) return static_cast<int64_t>(p.per_sample ? g * p.N : 0u) + i;
   const uint32_t b = p.per_sample ? g : fdiv(i, p.div_n);
   const uint32_t t = p.per_sample ? i : i - b * static_cast<uint32_t>(p.N);
   const uint32_t r = fdiv(t, p.div_nl);
   return static_cast<int64_t>(r * p.B + b) * p.Nl + (t - r * p.Nl);
 }
 
-// Sums of M values over a team of W warps (its warps' slots of `red`, which the
-// team's previous sums do not use), in warp order; every thread gets them.
+// Sums of M values over a team of W warps (through the team's 12 slots of M rows
+// of `red`, zero past the last warp, which the team's previous sums do not
+// use), in a fixed order; every thread gets them.
+constexpr int kLnTeamSlots = 12, kLnRed = 8 * kLnTeamSlots;  // (teams of several warps: 8 at most)
+
 template <int M>
-__device__ __forceinline__ void team_sums(float (&v)[M], float (*red)[kLnMaxWarps], int team, int W) {
+__device__ __forceinline__ void team_sums(float (&v)[M], float (*red)[kLnRed], int team, int W) {
 #pragma unroll
   for (int m = 0; m < M; ++m) v[m] = warp_sum(v[m]);
   if (W == 1) return;
+  const int base = team * kLnTeamSlots;
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int m = 0; m < M; ++m) red[m][threadIdx.x >> 5] = v[m];
+    for (int m = 0; m < M; ++m) red[m][base + (threadIdx.x >> 5) - team * W] = v[m];
   }
   asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * W) : "memory");
 #pragma unroll
   for (int m = 0; m < M; ++m) {
-    float t = 0.f;
-    for (int k = team * W; k < (team + 1) * W; ++k) t += red[m][k];
-    v[m] = t;
+    const float4 *t = reinterpret_cast<const float4 *>(&red[m][base]);
+    const float4 a = t[0], b = t[1], c = t[2];
+    v[m] = ((a.x + a.y) + (a.z + a.w)) + (((b.x + b.y) + (b.z + b.w)) + ((c.x + c.y) + (c.z + c.w)));
   }
+}
+
+__device__ __forceinline__ void clear_red(float *red) {
+  for (int k = threadIdx.x; k < 4 * kLnRed; k += blockDim.x) red[k] = 0.f;
 }
 
 // Parameter row `row` into shared memory in fp32; `none` where there is none.
@@ -205,10 +218,10 @@ __device__ __forceinline__ void ln_zero_padding(const LnParams &p, bool stats) {
 // registers, so that a large mean costs no digits.  Team i takes rows i,
 // i + teams, ... of group blockIdx.y.
 template <int V>
-__global__ void __launch_bounds__(32 * kLnMaxWarps, ln_blocks_per_sm(V, false))
+__global__ void __launch_bounds__(32 * ln_max_warps(V, false), ln_blocks_per_sm(V, false))
 layer_norm_kernel(const LnParams p, int W) {
   constexpr int K = kLnStages;
-  __shared__ float red[4][kLnMaxWarps];
+  __shared__ __align__(16) float red[4][kLnRed];
   extern __shared__ __align__(16) uint8_t ln_smem[];
   float4 *const sw = reinterpret_cast<float4 *>(ln_smem), *const sb = sw + 2 * p.C8;
   const int team = (threadIdx.x >> 5) / W, tn = 32 * W, tt = threadIdx.x - team * tn;
@@ -231,6 +244,7 @@ layer_norm_kernel(const LnParams p, int W) {
   for (int s = 0; s < K - 1; ++s) fetch(s, i + s * teams);
   ln_stage_params(p, p.weight, 1.f, p.per_sample ? g : 0, sw);
   ln_stage_params(p, p.bias, 0.f, p.per_sample ? g : 0, sb);
+  clear_red(red[0]);
   __syncthreads();
   int s = 0, ph = 0;
   for (; i < nrows; i += teams, ph ^= 2) {
@@ -289,12 +303,11 @@ layer_norm_kernel(const LnParams p, int W) {
 // Backward.  Each team keeps the gradient sums of its rows; a block's teams are
 // added in order, and the sums leave as one partial row per block, which
 // layer_norm_grad_kernel adds in block order: the result depends on no race.
-// Between the sums over a row and its result the row stays packed.
 template <int V, bool kGrad>
-__global__ void __launch_bounds__(32 * kLnMaxWarps, ln_blocks_per_sm(V, true))
+__global__ void __launch_bounds__(32 * ln_max_warps(V, true), ln_blocks_per_sm(V, true))
 layer_norm_backward_kernel(const LnParams p, int W) {
   constexpr int K = kLnStages;
-  __shared__ float red[4][kLnMaxWarps];
+  __shared__ __align__(16) float red[4][kLnRed];
   extern __shared__ __align__(16) uint8_t ln_smem[];
   // (the kernel that adds the partial rows may take its place meanwhile)
   asm volatile("griddepcontrol.launch_dependents;");
@@ -323,16 +336,17 @@ layer_norm_backward_kernel(const LnParams p, int W) {
 #pragma unroll
   for (int s = 0; s < K - 1; ++s) fetch(s, i + s * teams);
   int64_t row = 0;
-  float next_mean = 0.f, next_rstd = 0.f;
+  float rstd = 0.f, mean = 0.f;  // of the next row
   auto stats = [&](uint32_t j) {
     if (j < nrows) {
       row = ln_row(p, g, j);
-      next_mean = __ldg(p.mean_in + row);
-      next_rstd = __ldg(p.rstd_in + row);
+      mean = __ldg(p.mean_in + row);
+      rstd = __ldg(p.rstd_in + row);
     }
   };
   stats(i);
   ln_stage_params(p, p.weight, 1.f, p.per_sample ? g : 0, sw);
+  clear_red(red[0]);
   __syncthreads();
   const uint64_t zero2 = f2_pack(0.f, 0.f);
   uint64_t dw[V][4], db[V][4];
@@ -343,25 +357,37 @@ layer_norm_backward_kernel(const LnParams p, int W) {
   int s = 0, ph = 0;
   for (; i < nrows; i += teams, ph ^= 2) {
     cp_async_wait_group<K - 2>();
-    const uint64_t nmean2 = f2_pack(-next_mean, -next_mean), rstd2 = f2_pack(next_rstd, next_rstd);
+    // xh = x rstd + shift: one rounding more on the mean's share, like the
+    // mean's own
+    const float rs = rstd, shift = -mean * rstd;
+    const uint64_t rstd2 = f2_pack(rs, rs), shift2 = f2_pack(shift, shift);
     uint4 *dx = p.y + row * p.C8;
-    uint4 xp[V], dp[V];
+    // g stays in registers for the second sweep, or dy packed when V = 4
+    // (kept, its 16 registers spilled)
+    constexpr bool kKeep = V < 4;
+    uint4 xp[V], dk[kKeep ? 1 : V];
+    uint64_t gk[kKeep ? V : 1][4];
     uint64_t a1 = zero2, a2 = zero2;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = tt + v * tn;
       const bool in = c < p.C8;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      xp[v] = in ? ld_shared_v4(ring + s * line + 2 * v * vec) : zero;
-      dp[v] = in ? ld_shared_v4(ring + s * line + (2 * v + 1) * vec) : zero;
+      uint4 dp = make_uint4(0u, 0u, 0u, 0u);
+      xp[v] = dp;
+      if (in) {
+        xp[v] = ld_shared_v4(ring + s * line + 2 * v * vec);
+        dp = ld_shared_v4(ring + s * line + (2 * v + 1) * vec);
+      }
       uint64_t x[4], d[4], w[4];
       ln_unpack2(xp[v], x);
-      ln_unpack2(dp[v], d);
+      ln_unpack2(dp, d);
+      if (!kKeep) dk[kKeep ? 0 : v] = dp;
       ln_load_params(sw, p.C8, in ? c : 0, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t xh = f2_mul(f2_add(x[e], nmean2), rstd2);
+        const uint64_t xh = f2_fma(x[e], rstd2, shift2);
         const uint64_t gv = f2_mul(d[e], w[e]);   // (0 past the row)
+        if (kKeep) gk[kKeep ? v : 0][e] = gv;
         a1 = f2_add(a1, gv);
         a2 = f2_fma(gv, xh, a2);
         if (kGrad) {
@@ -375,21 +401,26 @@ layer_norm_backward_kernel(const LnParams p, int W) {
     stats(i + teams);  // in flight across the reduction
     float sums[2] = {f2_sum(a1), f2_sum(a2)};
     team_sums<2>(sums, red + ph, team, W);
-    const float s1 = -sums[0] * p.inv_c, s2 = -sums[1] * p.inv_c;
-    const uint64_t ns1 = f2_pack(s1, s1), ns2 = f2_pack(s2, s2);
+    // dx = rstd (g - s1 - xh s2) = g rstd + (x a + b)
+    const float s1 = sums[0] * p.inv_c, s2 = sums[1] * p.inv_c;
+    const float a = -rs * rs * s2, bb = -rs * fmaf(s2, shift, s1);
+    const uint64_t aa2 = f2_pack(a, a), bb2 = f2_pack(bb, bb);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = tt + v * tn;
       if (c < p.C8) {
-        uint64_t x[4], d[4], w[4];
+        uint64_t x[4], gv[4];
         ln_unpack2(xp[v], x);
-        ln_unpack2(dp[v], d);
-        ln_load_params(sw, p.C8, c, w);
+        if (!kKeep) {
+          uint64_t w[4];
+          ln_unpack2(dk[kKeep ? 0 : v], gv);
+          ln_load_params(sw, p.C8, c, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint64_t xh = f2_mul(f2_add(x[e], nmean2), rstd2);
-          x[e] = f2_mul(f2_fma(xh, ns2, f2_fma(d[e], w[e], ns1)), rstd2);
+          for (int e = 0; e < 4; ++e) gv[e] = f2_mul(gv[e], w[e]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = f2_fma(kKeep ? gk[kKeep ? v : 0][e] : gv[e], rstd2, f2_fma(x[e], aa2, bb2));
         dx[c] = ln_pack2(x);
       }
     }
