@@ -80,6 +80,8 @@ __device__ __forceinline__ int64_t bwd_row(const AttnBwdParams &p, int bh, int t
 template <int D>
 __global__ void __launch_bounds__(256) attention_delta_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+  // the main kernel's blocks may begin to fetch their tiles beside this one
+  asm volatile("griddepcontrol.launch_dependents;");
   const int64_t tiles = static_cast<int64_t>(p.BH) * p.T;
   if (blockIdx.x >= tiles) {
     const int pad = p.Np - p.N;
@@ -390,6 +392,8 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
           ok = wait(bar_stat_empty + 8 * s, ((j >> 1) & 1) ^ 1);
           if (!ok) break;
           if (lane == 0) {
+            // (written by the kernel in front of this one)
+            if (j == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
             mbar_arrive_expect_tx(bar_stat + 8 * s, 1024);
             bulk_load(sbase + C::kOffStat + s * 1024,
                       p.stat + (static_cast<int64_t>(bh) * T + j) * 256, 1024, bar_stat + 8 * s);
@@ -640,12 +644,13 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
     } else {
       // this thread's rows' statistics, both query tiles
       float nlse[2], ndelta[2];
+      asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const float *stat =
             p.stat + (static_cast<int64_t>(bh) * T + t0 / 128 + (t < nt ? t : 0)) * 256 + row;
-        nlse[t] = __ldg(stat);
-        ndelta[t] = __ldg(stat + 128);
+        nlse[t] = stat[0];
+        ndelta[t] = stat[128];
       }
       uint32_t par = 0;
       for (int j = 0; j < T && ok; ++j) {

@@ -940,9 +940,9 @@ sp_status launch_attention_backward(const CUtensorMap *m, const sp::AttnBwdParam
   if (st != SP_OK) return st;
   const unsigned ctas =
       static_cast<unsigned>(p.BH) * (p.T + (p.T + p.dq_tiles - 1) / p.dq_tiles);
-  sp::attention_backward_kernel<D><<<ctas, C::kThreads, C::kSmemBytes, cs>>>(m[0], m[1], m[2], m[3],
-                                                                             p);
-  return launch_status(cudaGetLastError());
+  return launch_status(launch_dependent(sp::attention_backward_kernel<D>, dim3(ctas),
+                                        dim3(C::kThreads), C::kSmemBytes, cs, m[0], m[1], m[2],
+                                        m[3], p));
 }
 
 sp_status attention_backward(const void *q, const void *k, const void *v, const void *o,
