@@ -361,6 +361,68 @@ def test_block_of_norm_projection_attention_and_back():
     assert sp.device_status() == sp.SP_OK
 
 
+@pytest.mark.parametrize("B,N,H,D,P", [(1, 700, 4, 128, 4), (2, 333, 6, 64, 3)])
+def test_ranks_of_the_multi_gpu_form(B, N, H, D, P):
+    """UlyssesRank's phases for P virtual ranks, the all-to-alls as copies:
+    bit-equal to the call on all shards (a row's arithmetic depends neither on
+    the layout nor on which heads a call holds); and one rank's whole step."""
+    shape = sp.Shape(B, N, H, D, P)
+    q, k, v, do = (_to_layout(t, "seq", P, 0.0) for t in _inputs(B, N, H, D, seed=6))
+    o, lse = torch.empty_like(q), torch.empty(shape.lse_shape, device="cuda")
+    sp.attention_seqsharded(q, k, v, o, shape, lse=lse)
+    want = [torch.empty_like(q) for _ in range(3)]
+    sp.attention_backward_seqsharded(q, k, v, o, lse, do, *want, shape)
+    ranks = [sp.UlyssesRank(shape) for _ in range(P)]
+
+    def exchange(sends):  # recv[r] = chunk r of every rank, in rank order
+        return [torch.stack([s[r] for s in sends]) for r in range(P)]
+
+    qkv = [exchange(list(s)) for s in zip(*[r.send_qkv(q[i], k[i], v[i]) for i, r in enumerate(ranks)])]
+    lses = [torch.empty(shape.head_group().lse_shape, device="cuda") for _ in ranks]
+    outs = [r.attend(*(t[i] for t in qkv), lse=lses[i]) for i, r in enumerate(ranks)]
+    dos = exchange([r.send_grad(do[i]) for i, r in enumerate(ranks)])
+    grads = [r.attend_backward(*(t[i] for t in qkv), outs[i], lses[i], dos[i])
+             for i, r in enumerate(ranks)]
+    backs = [exchange(list(g)) for g in zip(*grads)]
+    for i, r in enumerate(ranks):
+        got = r.finish_grads([b[i] for b in backs])
+        assert all(torch.equal(g, w[i]) for g, w in zip(got, want)), i
+    one = sp.Shape(B, N, H, D, 1)
+    x = [_to_layout(t, "seq", 1, 0.0)[0] for t in _inputs(B, N, H, D, seed=6)]
+    rank, lse = sp.UlyssesRank(one), torch.empty(one.lse_shape, device="cuda")
+    copy = lambda send, recv: recv.copy_(send)
+    rank.step(*x[:3], copy, lse=lse)
+    for g, w in zip(rank.backward_step(x[3], lse, copy), want):
+        assert torch.equal(g, _from_layout(w, "seq", B, N, H, D, P)[0])
+    assert sp.device_status() == sp.SP_OK
+
+
+@pytest.mark.parametrize("B,N,H,D,P", [(2049, 128, 64, 128, 1), (1025, 256, 64, 128, 2)])
+def test_offsets_past_32_bits(B, N, H, D, P):
+    """Tensors of more than 2^31 elements: the first and the last heads, by
+    the formula and against a call on them alone."""
+    shape = sp.Shape(B, N, H, D, P)
+    assert B * N * H * D > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v, do = (torch.empty(shape.seq_sharded, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+                   for _ in range(4))
+    o, lse = torch.empty_like(q), torch.empty(shape.lse_shape, device="cuda")
+    sp.attention_seqsharded(q, k, v, o, shape, lse=lse)
+    d = [torch.empty_like(q) for _ in range(3)]
+    sp.attention_backward_seqsharded(q, k, v, o, lse, do, *d, shape)
+    assert sp.device_status() == sp.SP_OK
+    small = sp.Shape(1, N, 2, D, P)
+    for b, h in ((0, 0), (B // 2, 30), (B - 1, H - 2)):
+        part = [t[:, b:b + 1, :, h:h + 2].contiguous() for t in (q, k, v, o, do)]
+        l = lse[b:b + 1, h:h + 2].contiguous()
+        w = [torch.empty_like(part[0]) for _ in range(3)]
+        sp.attention_backward_seqsharded(*part[:4], l, part[4], *w, small)
+        assert all(torch.equal(x[:, b:b + 1, :, h:h + 2], y) for x, y in zip(d, w))
+        logical = [_from_layout(t, "seq", 1, N, 2, D, P)[0] for t in part]
+        ref, err = _oracle(*logical[:4], l[..., :N], logical[4], 1 / math.sqrt(D))
+        _check(w, ref, err, "seq", small)
+
+
 def test_binding_refusals():
     B, N, H, D, P = 1, 100, 2, 128, 2
     shape = sp.Shape(B, N, H, D, P)

@@ -295,6 +295,46 @@ def test_outputs_stay_inside_their_buffers():
     _close(_unshard(v["dx"], N)[0], ref["dx"], ref["edx"], "bf16", "dx")
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the first and the last rows against the call on
+    them alone."""
+    B, N, C, P = 2, 140000, 8192, 1
+    assert B * N * C > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = (torch.empty(P, B, N, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+             for _ in range(2))
+    w = 1 + 0.3 * torch.randn(B, C, generator=g, device="cuda")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean = torch.empty(P, B, N, device="cuda")
+    rstd, dw, db = torch.empty_like(mean), torch.empty_like(w), torch.empty_like(w)
+    shape = _shape(B, N, P)
+    sp.layer_norm(x, w, w, y, shape, mean=mean, rstd=rstd)
+    sp.layer_norm_backward(dy, x, w, mean, rstd, dx, shape, dweight=dw, dbias=db)
+    for b, n in ((0, 0), (1, N - 40), (0, N - 40)):
+        part = x[:, b:b + 1, n:n + 40].contiguous()
+        pd = dy[:, b:b + 1, n:n + 40].contiguous()
+        yp, dxp = torch.empty_like(part), torch.empty_like(part)
+        m = torch.empty(1, 1, 40, device="cuda")
+        r = torch.empty_like(m)
+        sp.layer_norm(part, w[b], w[b], yp, _shape(1, 40, 1), mean=m, rstd=r)
+        sp.layer_norm_backward(pd, part, w[b], m, r, dxp, _shape(1, 40, 1))
+        assert torch.equal(y[:, b:b + 1, n:n + 40], yp) and torch.equal(rstd[:, b:b + 1, n:n + 40], r)
+        assert torch.equal(dx[:, b:b + 1, n:n + 40], dxp)
+    # the sums over all rows, in 64 bits by blocks of rows
+    ref_w, ref_b = torch.zeros(B, C, dtype=torch.float64, device="cuda"), torch.zeros(B, C, dtype=torch.float64, device="cuda")
+    abs_w = torch.zeros_like(ref_w)
+    for n in range(0, N, 4000):
+        d = dy[0, :, n:n + 4000].double()
+        xh = (x[0, :, n:n + 4000].double() - mean[0, :, n:n + 4000, None]) * rstd[0, :, n:n + 4000, None]
+        ref_w += (d * xh).sum(1)
+        ref_b += d.sum(1)
+        abs_w += (d * xh).abs().sum(1)
+    # a block's rows (up to N / 148 of a team) and the blocks' sums in fp32
+    depth = N / 148 + 200
+    assert ((dw - ref_w).abs() <= depth * U * abs_w).all()
+    assert ((db - ref_b).abs() <= depth * U * N * 6).all()
+
+
 def test_binding_refusals():
     B, N, C, P = 1, 10, 64, 1
     x, dy, w, b = _inputs(B, N, C, "shared_fp32", seed=1)

@@ -438,6 +438,14 @@ class UlyssesRank:
       -- all-to-all back --
       finish(back)        P returned chunks -> this rank's output shard
                           (sp_exchange_unpack)
+    and the way back, when attend was given an lse ([B][Hl][Np]) to keep:
+      send_grad(do)       the output's gradient shard -> [P][B][Nl][Hl][D]
+      -- all-to-all --
+      attend_backward(q, k, v, o, lse, do)
+                          the head group's three gradients in chunk order,
+                          from the received Q, K, V, attend's output and dO
+      -- three all-to-alls back --
+      finish_grads(back)  three returned chunk sets -> gradient shards
     Keeping the phases apart lets the caller choose the exchange (NCCL over
     NVLink, or a copy between virtual ranks on one GPU).  The buffers a phase
     returns belong to this object and are reused by the next step: each
@@ -476,13 +484,51 @@ class UlyssesRank:
         exchange_unpack(back, out, self.shape, stream)
         return out
 
-    def step(self, q, k, v, all_to_all):
+    def send_grad(self, do, stream=None):
+        send = self._buf("send_do", self.shape.send_chunks, do)
+        exchange_pack(do, send, self.shape, stream)
+        return send
+
+    def attend_backward(self, q, k, v, o, lse, do, stream=None):
+        group = self.shape.head_group()
+        grads = [self._buf(n, self.shape.send_chunks, q) for n in ("dq", "dk", "dv")]
+        torch = _torch()
+        ws = self._bufs.get("workspace")
+        if ws is None or ws.device != q.device:
+            ws = self._bufs["workspace"] = torch.empty(attention_backward_workspace(group),
+                                                       dtype=torch.uint8, device=q.device)
+        attention_backward_seqsharded(q, k, v, o, lse, do, *grads, group, workspace=ws,
+                                      stream=stream)
+        return grads
+
+    def finish_grads(self, back, stream=None):
+        out = []
+        for name, b in zip(("grad_q", "grad_k", "grad_v"), back):
+            out.append(self._buf(name, self.shape.rank_shard, b))
+            exchange_unpack(b, out[-1], self.shape, stream)
+        return out
+
+    def backward_step(self, do, lse, all_to_all):
+        """The way back of the last step, which was given this lse: returns the
+        gradients of its q, k and v shards (this object's buffers)."""
+        q, k, v = self.recv_buffers(do)
+        recv = self._buf("recv_do", self.shape.send_chunks, do)
+        all_to_all(self.send_grad(do), recv)
+        back = []
+        for name, g in zip(("back_dq", "back_dk", "back_dv"),
+                           self.attend_backward(q, k, v, self._bufs["o"], lse, recv)):
+            back.append(self._buf(name, self.shape.send_chunks, g))
+            all_to_all(g, back[-1])
+        return self.finish_grads(back)
+
+    def step(self, q, k, v, all_to_all, lse=None):
         """The whole step with all_to_all(send, recv) filling recv: returns
-        this rank's output shard (this object's buffer)."""
+        this rank's output shard (this object's buffer).  lse ([B][Hl][Np]
+        float32), if given, is filled for backward_step."""
         recv = self.recv_buffers(q)
         for send, r in zip(self.send_qkv(q, k, v), recv):
             all_to_all(send, r)
-        o = self.attend(*recv)
+        o = self.attend(*recv, lse=lse)
         back = self._buf("back", self.shape.send_chunks, o)
         all_to_all(o, back)
         return self.finish(back)
