@@ -54,9 +54,11 @@ struct LnParams {
 constexpr int kLnFwdVec = 6, kLnBwdVec = 4;  // vectors of a thread at most
 constexpr int kLnStages = 4;                 // rows of a team's ring
 // Warps of a block at most and blocks of an SM, by registers: 128 a thread (64
-// with few vectors) forward; 80, 128 or, from three vectors on, 168 backward.
+// with few vectors) forward; 80, 128, 168 or 200 backward, where more warps with
+// fewer registers were slower (5,120 columns, four vectors a thread: 420 us with
+// 10 warps' registers, 467 with 12 warps'; two vectors and 20 warps 530).
 __host__ __device__ constexpr int ln_max_warps(int V, bool backward) {
-  return backward && V != 2 ? 12 : 16;
+  return !backward || V == 2 ? 16 : V == 4 ? 10 : 12;
 }
 __host__ __device__ constexpr int ln_blocks_per_sm(int V, bool backward) {
   return V <= (backward ? 1 : 2) ? 2 : 1;
