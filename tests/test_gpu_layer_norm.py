@@ -121,7 +121,9 @@ CASES = [
     (1, 31, 1, 3968, "shared_bf16"), (2, 19, 2, 5120, "sample_fp32"), (1, 9, 1, 8192, "shared_fp32"),
     (2, 13, 2, 8184, "sample_bf16"), (2, 700, 2, 6400, "shared_fp32"), (1, 900, 3, 7160, "shared_bf16"),
     (3, 411, 2, 2816, "sample_fp32"), (2, 1500, 4, 5120, "shared_fp32"), (1, 2000, 1, 4096, "shared_bf16"),
-    (2, 1333, 2, 1536, "shared_bf16"), (300, 5, 2, 72, "sample_fp32"), (1, 3000, 2, 256, "shared_fp32"), (1, 2500, 1, 32, "none"),
+    (2, 1333, 2, 1536, "shared_bf16"), (300, 5, 2, 72, "sample_fp32"),
+    (1, 5001, 2, 8, "shared_fp32"), (2, 9001, 4, 32, "shared_bf16"), (3, 7, 2, 56, "sample_fp32"),
+    (1, 40001, 1, 128, "shared_fp32"), (2, 20000, 3, 248, "sample_bf16"), (1, 3000, 2, 256, "shared_fp32"), (1, 2500, 1, 32, "none"),
 ]
 
 

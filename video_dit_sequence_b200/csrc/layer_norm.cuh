@@ -110,12 +110,6 @@ __device__ __forceinline__ void ln_param8(const void *base, int f32, int64_t row
   }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
 // Rows of one group of a pass, in the order of the logical sequence (so that
 // sums do not depend on P): i-th valid row of all samples, or of sample `g`
 // when every sample has its own parameters.
@@ -127,22 +121,27 @@ __device__ __forceinline__ int64_t ln_row(const LnParams &p, uint32_t g, uint32_
   return static_cast<int64_t>(r * p.B + b) * p.Nl + (t - r * p.Nl);
 }
 
-// Sums of M values over a team of W warps (through the team's 12 slots of M rows
-// of `red`, zero past the last warp, which the team's previous sums do not
-// use), in a fixed order; every thread gets them.
+// Sums of M values over a team of tn threads, in a fixed order; every thread gets
+// them.  kSub: tn is at most 32, a power of two; else whole warps (through the
+// team's 12 slots of M rows of `red`, zero past the last warp, which the team's
+// previous sums do not use).
 constexpr int kLnTeamSlots = 12, kLnRed = 8 * kLnTeamSlots;  // (teams of several warps: 8 at most)
 
-template <int M>
-__device__ __forceinline__ void team_sums(float (&v)[M], float (*red)[kLnRed], int team, int W) {
+template <int M, bool kSub>
+__device__ __forceinline__ void team_sums(float (&v)[M], float (*red)[kLnRed], int team, int tn) {
 #pragma unroll
-  for (int m = 0; m < M; ++m) v[m] = warp_sum(v[m]);
-  if (W == 1) return;
+  for (int d = 16; d > 0; d >>= 1)
+    if (!kSub || d < tn) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], d);
+    }
+  if (kSub || tn == 32) return;
   const int base = team * kLnTeamSlots;
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int m = 0; m < M; ++m) red[m][base + (threadIdx.x >> 5) - team * W] = v[m];
+    for (int m = 0; m < M; ++m) red[m][base + ((threadIdx.x - team * tn) >> 5)] = v[m];
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * W) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tn) : "memory");
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     const float4 *t = reinterpret_cast<const float4 *>(&red[m][base]);
@@ -221,12 +220,14 @@ __device__ __forceinline__ void ln_zero_padding(const LnParams &p, bool stats) {
 // i + teams, ... of group blockIdx.y.
 template <int V>
 __global__ void __launch_bounds__(32 * ln_max_warps(V, false), ln_blocks_per_sm(V, false))
-layer_norm_kernel(const LnParams p, int W) {
+layer_norm_kernel(const LnParams p, int tn) {
   constexpr int K = kLnStages;
+  constexpr bool kSub = V == 1;
   __shared__ __align__(16) float red[4][kLnRed];
   extern __shared__ __align__(16) uint8_t ln_smem[];
   float4 *const sw = reinterpret_cast<float4 *>(ln_smem), *const sb = sw + 2 * p.C8;
-  const int team = (threadIdx.x >> 5) / W, tn = 32 * W, tt = threadIdx.x - team * tn;
+  const int team = threadIdx.x / tn, tt = threadIdx.x - team * tn;
+  const uint32_t sub = kSub ? (threadIdx.x & 31) / tn : 0;  // team of the warp
   const uint32_t g = blockIdx.y;
   const uint32_t nrows = p.per_sample ? p.N : p.B * p.N;  // below 2^31
   const uint32_t block_teams = blockDim.x / tn, teams = gridDim.x * block_teams;
@@ -249,14 +250,15 @@ layer_norm_kernel(const LnParams p, int W) {
   clear_red(red[0]);
   __syncthreads();
   int s = 0, ph = 0;
-  for (; i < nrows; i += teams, ph ^= 2) {
+  for (; i - sub < nrows; i += teams, ph ^= 2) {  // (the same steps in all lanes)
     cp_async_wait_group<K - 2>();
+    const bool row_in = !kSub || i < nrows;
     uint64_t f[V][4];
     uint64_t acc = f2_pack(0.f, 0.f), acc2 = acc;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      ln_unpack2(tt + v * tn < p.C8 ? ld_shared_v4(ring + s * line + v * vec)
-                                    : make_uint4(0u, 0u, 0u, 0u), f[v]);
+      ln_unpack2(row_in && tt + v * tn < p.C8 ? ld_shared_v4(ring + s * line + v * vec)
+                                              : make_uint4(0u, 0u, 0u, 0u), f[v]);
       acc = f2_add(acc, f2_add(f[v][0], f[v][1]));
       acc2 = f2_add(acc2, f2_add(f[v][2], f[v][3]));
     }
@@ -264,7 +266,7 @@ layer_norm_kernel(const LnParams p, int W) {
     fetch(s == 0 ? K - 1 : s - 1, i + (K - 1) * teams);
     s = s + 1 == K ? 0 : s + 1;
     float sum[1] = {f2_sum(f2_add(acc, acc2))};
-    team_sums<1>(sum, red + ph, team, W);
+    team_sums<1, kSub>(sum, red + ph, team, tn);
     const float mean = sum[0] * p.inv_c;
     const uint64_t nmean2 = f2_pack(-mean, -mean);
     acc = acc2 = f2_pack(0.f, 0.f);
@@ -278,7 +280,8 @@ layer_norm_kernel(const LnParams p, int W) {
       }
     }
     sum[0] = f2_sum(f2_add(acc, acc2));
-    team_sums<1>(sum, red + ph + 1, team, W);
+    team_sums<1, kSub>(sum, red + ph + 1, team, tn);
+    if (!row_in) continue;
     const float rstd = 1.0f / sqrtf(sum[0] * p.inv_c + p.eps);
     const uint64_t rstd2 = f2_pack(rstd, rstd);
     const int64_t row = ln_row(p, g, i);
@@ -307,14 +310,16 @@ layer_norm_kernel(const LnParams p, int W) {
 // layer_norm_grad_kernel adds in block order: the result depends on no race.
 template <int V, bool kGrad>
 __global__ void __launch_bounds__(32 * ln_max_warps(V, true), ln_blocks_per_sm(V, true))
-layer_norm_backward_kernel(const LnParams p, int W) {
+layer_norm_backward_kernel(const LnParams p, int tn) {
   constexpr int K = kLnStages;
+  constexpr bool kSub = V == 1;
   __shared__ __align__(16) float red[4][kLnRed];
   extern __shared__ __align__(16) uint8_t ln_smem[];
   // (the kernel that adds the partial rows may take its place meanwhile)
   asm volatile("griddepcontrol.launch_dependents;");
   float4 *const sw = reinterpret_cast<float4 *>(ln_smem);
-  const int team = (threadIdx.x >> 5) / W, tn = 32 * W, tt = threadIdx.x - team * tn;
+  const int team = threadIdx.x / tn, tt = threadIdx.x - team * tn;
+  const uint32_t sub = kSub ? (threadIdx.x & 31) / tn : 0;  // team of the warp
   const uint32_t g = blockIdx.y;
   const uint32_t nrows = p.per_sample ? p.N : p.B * p.N;  // below 2^31
   const uint32_t block_teams = blockDim.x / tn, teams = gridDim.x * block_teams;
@@ -340,6 +345,7 @@ layer_norm_backward_kernel(const LnParams p, int W) {
   int64_t row = 0;
   float rstd = 0.f, mean = 0.f;  // of the next row
   auto stats = [&](uint32_t j) {
+    mean = rstd = 0.f;
     if (j < nrows) {
       row = ln_row(p, g, j);
       mean = __ldg(p.mean_in + row);
@@ -357,8 +363,9 @@ layer_norm_backward_kernel(const LnParams p, int W) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw[v][e] = db[v][e] = zero2;
   int s = 0, ph = 0;
-  for (; i < nrows; i += teams, ph ^= 2) {
+  for (; i - sub < nrows; i += teams, ph ^= 2) {  // (the same steps in all lanes)
     cp_async_wait_group<K - 2>();
+    const bool row_in = !kSub || i < nrows;
     // xh = x rstd + shift: one rounding more on the mean's share, like the
     // mean's own
     const float rs = rstd, shift = -mean * rstd;
@@ -373,7 +380,7 @@ layer_norm_backward_kernel(const LnParams p, int W) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = tt + v * tn;
-      const bool in = c < p.C8;
+      const bool in = row_in && c < p.C8;
       uint4 dp = make_uint4(0u, 0u, 0u, 0u);
       xp[v] = dp;
       if (in) {
@@ -402,7 +409,8 @@ layer_norm_backward_kernel(const LnParams p, int W) {
     s = s + 1 == K ? 0 : s + 1;
     stats(i + teams);  // in flight across the reduction
     float sums[2] = {f2_sum(a1), f2_sum(a2)};
-    team_sums<2>(sums, red + ph, team, W);
+    team_sums<2, kSub>(sums, red + ph, team, tn);
+    if (!row_in) continue;
     // dx = rstd (g - s1 - xh s2) = g rstd + (x a + b)
     const float s1 = sums[0] * p.inv_c, s2 = sums[1] * p.inv_c;
     const float a = -rs * rs * s2, bb = -rs * fmaf(s2, shift, s1);
@@ -428,12 +436,21 @@ layer_norm_backward_kernel(const LnParams p, int W) {
     }
   }
   if (kGrad) {
-    // the block's teams in order, through the ring: [dw, db][half][C8] float4
+    // the warps' teams, then the block's warps (or larger teams) in order,
+    // through the ring: [dw, db][half][C8] float4
     cp_async_wait_group<0>();
+    if (kSub)
+      for (int d = tn; d < 32; d <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dw[0][e] = f2_add(dw[0][e], __shfl_xor_sync(0xffffffffu, dw[0][e], d));
+          db[0][e] = f2_add(db[0][e], __shfl_xor_sync(0xffffffffu, db[0][e], d));
+        }
+    const int turns = blockDim.x / max(tn, 32), turn = kSub ? threadIdx.x >> 5 : team;
     ulonglong2 *acc = reinterpret_cast<ulonglong2 *>(sw + 2 * p.C8);
-    for (uint32_t k = 0; k < block_teams; ++k) {
+    for (int k = 0; k < turns; ++k) {
       __syncthreads();
-      if (static_cast<uint32_t>(team) != k) continue;
+      if (turn != k || sub != 0) continue;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = tt + v * tn;

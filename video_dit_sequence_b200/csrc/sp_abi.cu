@@ -766,11 +766,11 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 constexpr int kNormMaxSmem = 224 * 1024;
 
-// How a layer norm pass is spread: warps of a team (which takes a row), vectors
-// of a thread, teams of a block.  Blocks of a group: as many as the 148 SMs
+// How a layer norm pass is spread: warps and threads of a team (which takes a
+// row), vectors of a thread, teams of a block.  Blocks of a group: as many as the 148 SMs
 // hold at once; few rows are spread over all SMs.
 struct NormPlan {
-  int W, V, threads, smem, groups;
+  int W, V, team, threads, smem, groups;
   int64_t blocks;  // of a group
 };
 
@@ -791,15 +791,20 @@ NormPlan norm_plan(const sp::LnParams &p, bool backward) {
   const int64_t nrows = p.per_sample ? p.N : static_cast<int64_t>(p.B) * p.N;
   const int64_t slots =
       std::max<int64_t>(1, 148 * sp::ln_blocks_per_sm(pl.V, backward) / pl.groups);
-  int64_t teams = std::max<int64_t>(
-      1, std::min<int64_t>(teams_of(pl.W), (nrows + slots - 1) / slots));
+  // a row of few vectors takes a part of a warp
+  pl.team = 32 * pl.W;
+  while (pl.V == 1 && pl.W == 1 && pl.team / 2 >= p.C8) pl.team /= 2;
+  const int unit = std::max(1, 32 / pl.team);  // teams of a warp
+  const int64_t wanted = (std::min<int64_t>(static_cast<int64_t>(teams_of(pl.W)) * unit,
+                                            (nrows + slots - 1) / slots) + unit - 1) / unit;
+  int64_t teams = std::max<int64_t>(1, wanted) * unit;
   // parameters (weight and bias, or weight) and the rings; the backward pass
   // adds its teams' gradient sums in the rings' place
-  for (;; --teams) {
-    pl.threads = static_cast<int>(teams) * pl.W * 32;
+  for (;; teams -= unit) {
+    pl.threads = static_cast<int>(teams) * pl.team;
     const int ring = sp::kLnStages * (backward ? 2 : 1) * pl.V * pl.threads * 16;
     pl.smem = (backward ? 32 : 64) * p.C8 + std::max(ring, backward ? 64 * p.C8 : 0);
-    if (pl.smem <= kNormMaxSmem || teams == 1) break;
+    if (pl.smem <= kNormMaxSmem || teams == unit) break;
   }
   pl.blocks = std::min((nrows + teams - 1) / teams, slots);
   return pl;
@@ -839,7 +844,7 @@ sp_status layer_norm(const void *x, const void *weight, const void *bias, void *
     const auto kernel = sp::layer_norm_kernel<decltype(v)::value>;
     const cudaError_t e = set_smem_once(kernel, kNormMaxSmem, set);
     if (e != cudaSuccess) return e;
-    kernel<<<dim3(static_cast<unsigned>(pl.blocks), pl.groups), pl.threads, pl.smem, cs>>>(p, pl.W);
+    kernel<<<dim3(static_cast<unsigned>(pl.blocks), pl.groups), pl.threads, pl.smem, cs>>>(p, pl.team);
     return cudaGetLastError();
   }));
 }
@@ -860,7 +865,7 @@ cudaError_t launch_norm_backward(const sp::LnParams &p, const NormPlan &pl, cuda
   const auto kernel = sp::layer_norm_backward_kernel<V, kGrad>;
   const cudaError_t e = set_smem_once(kernel, kNormMaxSmem, set);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(static_cast<unsigned>(pl.blocks), pl.groups), pl.threads, pl.smem, cs>>>(p, pl.W);
+  kernel<<<dim3(static_cast<unsigned>(pl.blocks), pl.groups), pl.threads, pl.smem, cs>>>(p, pl.team);
   return cudaGetLastError();
 }
 
