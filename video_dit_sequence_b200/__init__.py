@@ -171,11 +171,11 @@ class Shape:
     def Np(self) -> int:
         return self.Nl * self.P
 
-    @property
+    @functools.cached_property
     def seq_sharded(self):
         return (self.P, self.B, self.Nl, self.H, self.D)
 
-    @property
+    @functools.cached_property
     def head_sharded(self):
         return (self.P, self.B, self.Np, self.Hl, self.D)
 
@@ -194,7 +194,7 @@ class Shape:
         over the whole sequence, still in P token shards."""
         return Shape(self.B, self.N, self.Hl, self.D, self.P, self.scale)
 
-    @property
+    @functools.cached_property
     def lse_shape(self):
         return (self.B, self.H, self.Np)
 
@@ -203,8 +203,13 @@ class Shape:
         """Q/K scale blocks of the FP8 call: ceil(N / FP8_BLOCK)."""
         return -(-self.N // FP8_BLOCK)
 
-    def c(self) -> sp_shape:
+    @functools.cached_property
+    def _c(self) -> sp_shape:
         return sp_shape(self.B, self.N, self.H, self.D, self.P, float(self.scale))
+
+    def c(self) -> sp_shape:
+        """The C struct (one per Shape, which the library only reads)."""
+        return self._c
 
 
 def padded_tokens(N: int, P: int) -> int:
