@@ -298,6 +298,42 @@ def _same_device(*tensors):
     return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+def _operands(device, *specs):
+    """Addresses of (tensor, shape, name, dtype) operands, all on `device`."""
+    torch = _torch()
+    Tensor, out = torch.Tensor, []
+    for t, shape, name, dtype in specs:
+        if t is None:
+            out.append(None)
+        elif (isinstance(t, Tensor) and t.device == device and t.dtype == dtype and
+              t.shape == shape and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            out.append(_ptr(t, shape, name, dtype))
+            if t.device != device:
+                raise ValueError(f"operands on several devices: {t.device}, {device}")
+    return out
+
+
+def _device_of(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call(fn, where, device, *args):
+    """Runs a library call with `device` current."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != SP_OK:
+        raise SpError(status, where)
+
+
 def _check(status: int, where: str):
     if status != SP_OK:
         raise SpError(status, where)
@@ -600,19 +636,19 @@ def attention_backward_workspace(shape: Shape) -> int:
 
 def _attention_backward(name, ts, q, k, v, o, lse, do, dq, dk, dv, shape, workspace, stream):
     torch = _torch()
-    s = shape.c()
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"),
-                 (dk, "dk"), (dv, "dv"), (q if workspace is None else workspace, "workspace")):
-        if not isinstance(t, torch.Tensor):
+    bf16, dev = torch.bfloat16, _device_of(q, "q")
+    for t, n in ((k, "k"), (v, "v"), (o, "o"), (lse, "lse"), (do, "do"), (dq, "dq"), (dk, "dk"),
+                 (dv, "dv")):
+        if t is None:
             raise TypeError(f"{n} must be a CUDA tensor")
-    with _same_device(q, k, v, o, lse, do, dq, dk, dv, workspace):
-        st = _stream(stream, q.device)
-        ws = _workspace(workspace, attention_backward_workspace(shape), q.device, stream)
-        _check(getattr(load(), name)(
-            _ptr(q, ts, "q"), _ptr(k, ts, "k"), _ptr(v, ts, "v"), _ptr(o, ts, "o"),
-            _ptr(lse, shape.lse_shape, "lse", torch.float32), _ptr(do, ts, "do"),
-            _ptr(dq, ts, "dq"), _ptr(dk, ts, "dk"), _ptr(dv, ts, "dv"),
-            ws.data_ptr(), ctypes.byref(s), st), name)
+    need = attention_backward_workspace(shape)   # (refuses a shape out of range)
+    ops = _operands(dev, (q, ts, "q", bf16), (k, ts, "k", bf16), (v, ts, "v", bf16),
+                    (o, ts, "o", bf16), (lse, shape.lse_shape, "lse", torch.float32),
+                    (do, ts, "do", bf16), (dq, ts, "dq", bf16), (dk, ts, "dk", bf16),
+                    (dv, ts, "dv", bf16))
+    st = _stream(stream, dev)
+    ws = _workspace(workspace, need, dev, stream)
+    _call(getattr(load(), name), name, dev, *ops, ws.data_ptr(), ctypes.byref(shape.c()), st)
 
 
 def attention_backward(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None, stream=None):
@@ -646,11 +682,12 @@ def _workspace(workspace, nbytes, device, stream):
             return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
+    if workspace.device != device:
+        raise ValueError(f"operands on several devices: {workspace.device}, {device}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    if workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
-                         f"{nbytes} needed")
+    if workspace.nbytes < nbytes:
+        raise ValueError(f"workspace holds {workspace.nbytes} bytes, {nbytes} needed")
     return workspace
 
 
@@ -668,7 +705,7 @@ def _norm_params(params, shape: Shape, hidden: int):
         raise TypeError(f"layer norm parameters must be bfloat16 or float32, got {t.dtype}")
     pshape = (hidden,) if t.dim() == 1 else (shape.B, hidden)
     for o in given:
-        if o.dtype != t.dtype or tuple(o.shape) != pshape:
+        if o.dtype != t.dtype or o.shape != pshape:
             raise ValueError(f"layer norm parameters must all be {t.dtype} of shape ({hidden},) or "
                              f"({shape.B}, {hidden}), got {o.dtype} {tuple(o.shape)}")
     return int(t.dim() == 2), int(t.dtype == torch.float32), t.dtype, pshape
@@ -682,17 +719,16 @@ def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: floa
     receive the rows' statistics (float32 [P][B][Nl]) for the backward
     pass."""
     torch = _torch()
-    hidden = int(x.shape[-1])
-    rows = shape.seq_sharded[:3]
+    dev = _device_of(x, "x")
+    hidden = x.shape[-1]
+    bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
+    full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, bias), shape, hidden)
-    s = shape.c()
-    with _same_device(x, weight, bias, y, mean, rstd):
-        _check(load().sp_layer_norm(
-            _ptr(x, rows + (hidden,), "x"), _ptr(weight, pshape, "weight", dtype),
-            _ptr(bias, pshape, "bias", dtype), _ptr(y, rows + (hidden,), "y"),
-            _ptr(mean, rows, "mean", torch.float32), _ptr(rstd, rows, "rstd", torch.float32),
-            hidden, float(eps), layout, ptype, ctypes.byref(s), _stream(stream, x.device)),
-            "sp_layer_norm")
+    ops = _operands(dev, (x, full, "x", bf16), (weight, pshape, "weight", dtype),
+                    (bias, pshape, "bias", dtype), (y, full, "y", bf16), (mean, rows, "mean", f32),
+                    (rstd, rows, "rstd", f32))
+    _call(load().sp_layer_norm, "sp_layer_norm", dev, *ops, hidden, float(eps), layout, ptype,
+          ctypes.byref(shape.c()), _stream(stream, dev))
 
 
 @functools.lru_cache(maxsize=256)
@@ -713,23 +749,21 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=Non
     least layer_norm_backward_workspace bytes to reuse (one per call in
     flight), else a fresh one."""
     torch = _torch()
-    hidden = int(x.shape[-1])
-    rows = shape.seq_sharded[:3]
+    dev = _device_of(x, "x")
+    hidden = x.shape[-1]
+    bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
+    full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, dweight, dbias), shape, hidden)
-    s = shape.c()
-    with _same_device(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace):
-        st = _stream(stream, x.device)
-        ws = None
-        if dweight is not None or dbias is not None:
-            ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden), x.device,
-                            stream)
-        _check(load().sp_layer_norm_backward(
-            _ptr(dy, rows + (hidden,), "dy"), _ptr(x, rows + (hidden,), "x"),
-            _ptr(weight, pshape, "weight", dtype), _ptr(mean, rows, "mean", torch.float32),
-            _ptr(rstd, rows, "rstd", torch.float32), _ptr(dx, rows + (hidden,), "dx"),
-            _ptr(dweight, pshape, "dweight", dtype), _ptr(dbias, pshape, "dbias", dtype),
-            None if ws is None else ws.data_ptr(), hidden, layout, ptype,
-            ctypes.byref(s), st), "sp_layer_norm_backward")
+    ops = _operands(dev, (dy, full, "dy", bf16), (x, full, "x", bf16),
+                    (weight, pshape, "weight", dtype), (mean, rows, "mean", f32),
+                    (rstd, rows, "rstd", f32), (dx, full, "dx", bf16),
+                    (dweight, pshape, "dweight", dtype), (dbias, pshape, "dbias", dtype))
+    st = _stream(stream, dev)
+    ws = None
+    if dweight is not None or dbias is not None:
+        ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden), dev, stream)
+    _call(load().sp_layer_norm_backward, "sp_layer_norm_backward", dev, *ops,
+          None if ws is None else ws.data_ptr(), hidden, layout, ptype, ctypes.byref(shape.c()), st)
 
 
 SPARSE_CUBE = 64         # SP_SPARSE_CUBE
