@@ -10,10 +10,16 @@
 // Five products of N x N x D per head.  dK and dV sum over queries, dQ over
 // keys: one of the two has to leave its CTA.  A single pass that adds 128 x 128
 // fp32 tiles of dQ to global memory in key order (which repeats bit for bit)
-// moves 64 KB out of every SM per tile, and was bound by it: 18.5 ms at 480p.
-// Here scores and dP are computed twice instead, seven products, and every sum
-// stays in tensor memory; results repeat bit for bit and depend neither on
-// timing nor on P.
+// moves 64 KB out of every SM per tile; it took 18.5 ms at 480p (12 heads,
+// 32,760 tokens) and 1.52 ms at 4,096 tokens x 40 heads.  Here scores and dP are
+// computed twice instead, seven products, and every sum stays in tensor memory:
+// 18.0 and 1.06 ms.  Results repeat bit for bit and depend neither on timing nor
+// on P.
+// What bounds it: at 480p the 1,000 W power cap (1.5 GHz of 1.97; seven products
+// at 1.28 PFLOP/s, cuBLAS holds 1.38 there).  A 128 x 128 tile takes 2,700 cycles
+// in a dK/dV CTA (its four products 2,048) and 2,050 in a dQ CTA (1,536); a
+// polynomial for part of the exponentials brought that to 2,450 and 1,970, and
+// the time, at the cap, not at all.  Short problems are bound by a CTA's chain.
 //
 // One launch holds both kinds of CTA:
 //   dK, dV: 128 keys; walks the 128-query tiles.  Scores are computed
@@ -156,65 +162,6 @@ struct AttnBwdCfg {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(r));
-  return r != 0;
-}
-
-// Untiled bulk copy global -> shared (16-byte aligned, multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// Asynchronous 16-byte copy global -> shared; bytes = 0 writes zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-// All of this thread's cp_async16 are complete.
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// Matrix products of bf16 operands whose descriptors differ from one another
-// only in the low word: high word = stride 1,024 bytes, version 1, 128-byte
-// swizzle (make_sdesc_sw128).
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-
-__device__ __forceinline__ void umma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void umma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-
 // Blocks of a head: its dQ pairs of query tiles first (they run longest), then
 // its key tiles; the CTAs that run together belong to one or two heads, whose
 // Q, K, V and dO stay in L2.
@@ -322,7 +269,7 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       // 16-byte chunk cc of row r at chunk cc ^ (r mod 8) of its column block,
       // as the TMA writes it.  Asynchronous copies keep the whole tile in
       // flight; with loads through registers, four at a time, a tile took
-      // 6 us (777 tokens in 3 shards, 2 x 6 heads: 220 instead of TODO us).
+      // 6 us (777 tokens in 3 shards, 2 x 6 heads: 220 instead of 44 us).
       auto copy_tile = [&](const uint8_t *base, uint32_t dst, int tok) {
         constexpr int kChunks = D / 8, kStep = 32 / kChunks;
         const int cc = lane % kChunks;
