@@ -258,6 +258,47 @@ def test_streams_workspaces_and_graphs():
     assert sp.device_status() == sp.SP_OK
 
 
+def test_beside_other_kernels():
+    """The forward pass and the norm on other streams at the same time (D = 64:
+    a CTA of each fits an SM's shared memory, and one waits for the other's
+    tensor memory), and one workspace in two graphs replayed in turn."""
+    B, N, H, D, P = 1, 3000, 16, 64, 1
+    shape = sp.Shape(B, N, H, D, P)
+    q, k, v, do = (_to_layout(t, "seq", P, 0.0) for t in _inputs(B, N, H, D, seed=9))
+    o, lse = torch.empty_like(q), torch.empty(shape.lse_shape, device="cuda")
+    sp.attention_seqsharded(q, k, v, o, shape, lse=lse)
+    want = [torch.empty_like(q) for _ in range(3)]
+    sp.attention_backward_seqsharded(q, k, v, o, lse, do, *want, shape)
+    x = q.view(P, B, N, H * D)
+    norm = torch.empty_like(x)
+    sp.layer_norm(x, None, None, norm, shape)
+    s = [torch.cuda.Stream() for _ in range(3)]
+    d = [torch.empty_like(q) for _ in range(3)]
+    o2, n2 = torch.empty_like(o), torch.empty_like(norm)
+    torch.cuda.synchronize()
+    for _ in range(8):
+        sp.attention_backward_seqsharded(q, k, v, o, lse, do, *d, shape, stream=s[0])
+        sp.attention_seqsharded(q, k, v, o2, shape, stream=s[1])
+        sp.layer_norm(x, None, None, n2, shape, stream=s[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(d + [o2, n2], want + [o, norm]))
+    ws = torch.empty(sp.attention_backward_workspace(shape), dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for t in ((q, k, v, o, lse, do), (q, k, v, o, lse, 2 * do)):
+        outs.append([torch.empty_like(q) for _ in range(3)])
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            sp.attention_backward_seqsharded(*t, *outs[-1], shape, workspace=ws)
+    for _ in range(3):
+        for gr in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], want))
+    # twice dO: every gradient doubles exactly
+    assert all(torch.equal(a, 2 * b) for a, b in zip(outs[1], want))
+    assert sp.device_status() == sp.SP_OK
+
+
 def _saved(d, shape):
     q, k, v, o, lse, do = d
     t = [_to_layout(x, "seq", shape.P) for x in (q, k, v, o, do)]

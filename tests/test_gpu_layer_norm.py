@@ -297,6 +297,51 @@ def test_outputs_stay_inside_their_buffers():
     _close(_unshard(v["dx"], N)[0], ref["dx"], ref["edx"], "bf16", "dx")
 
 
+def test_every_hidden_size():
+    """Every hidden size (the teams' warps, vectors and shared memory follow
+    from it) with enough rows for full blocks: y, the statistics and dx of a
+    few rows, and dweight, in 64 bits."""
+    N = 2500
+    g = torch.Generator(device="cuda").manual_seed(7)
+    big = torch.randn(N * 8192, generator=g, device="cuda").to(torch.bfloat16)
+    bigd = torch.randn(N * 8192, generator=g, device="cuda").to(torch.bfloat16)
+    rows = torch.tensor([0, 1, 147, 1201, N - 2, N - 1], device="cuda")
+    for C in range(8, sp.NORM_MAX_HIDDEN + 1, 8):
+        x, dy = (t[:N * C].view(1, 1, N, C) for t in (big, bigd))
+        w = (1 + 0.3 * torch.randn(C, generator=g, device="cuda"))
+        b = 0.3 * torch.randn(C, generator=g, device="cuda")
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        mean = torch.empty(1, 1, N, device="cuda")
+        rstd, dw, db = torch.empty_like(mean), torch.empty_like(w), torch.empty_like(w)
+        shape = _shape(1, N, 1)
+        sp.layer_norm(x, w, b, y, shape, mean=mean, rstd=rstd)
+        sp.layer_norm_backward(dy, x, w, mean, rstd, dx, shape, dweight=dw, dbias=db)
+        ref = _oracle(x[0, :, rows], dy[0, :, rows], w, b)
+        for got, name, kind in ((y, "y", "bf16"), (mean, "mean", "fp32"), (rstd, "rstd", "fp32"),
+                                (dx, "dx", "bf16")):
+            _close(got[0, :, rows], ref[name], ref["e" + name], kind, (C, name))
+        xd, d = x[0, 0].float(), dy[0, 0].float()   # (fp32 products, summed in 64 bits)
+        xh = (xd - mean[0, 0, :, None]) * rstd[0, 0, :, None]
+        terms = d * xh
+        assert ((dw - terms.sum(0, dtype=torch.float64)).abs()
+                <= DEPTH * U * (terms.abs().sum(0, dtype=torch.float64) + d.abs().sum(0))).all(), C
+        assert ((db - d.sum(0, dtype=torch.float64)).abs() <= DEPTH * U * d.abs().sum(0)).all(), C
+
+
+def test_rows_that_are_not_finite_stay_alone():
+    x, dy, w, b = _inputs(1, 50, 1160, "shared_fp32", seed=13)
+    xs, y0, _, _ = _forward(x, w, b, 1)
+    x[0, 20, 3] = float("nan")
+    x[0, 31, 7] = float("inf")
+    xs, y, mean, rstd = _forward(x, w, b, 1)
+    dx, dw, db = _backward(xs, dy, w, mean, rstd, 50, 1)
+    bad = torch.zeros(50, dtype=torch.bool, device="cuda")
+    bad[[20, 31]] = True
+    assert torch.isnan(y[0, 0][bad]).any(1).all() and torch.equal(y[0, 0][~bad], y0[0, 0][~bad])
+    assert torch.isnan(dx[0, 0][bad]).any(1).all() and torch.isfinite(dx[0, 0][~bad]).all()
+    assert torch.isnan(dw).any() and torch.isfinite(db).all()
+
+
 def test_offsets_past_32_bits():
     """More than 2^31 elements: the first and the last rows against the call on
     them alone."""

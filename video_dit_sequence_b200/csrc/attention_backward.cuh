@@ -104,11 +104,15 @@ __global__ void __launch_bounds__(256) attention_delta_kernel(const __grid_const
   const int qt = blockIdx.x % p.T, bh = blockIdx.x / p.T;
   const int c = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
   uint4 vo[128 / kRows], vd[128 / kRows];
+  float lse[128 / kRows];
 #pragma unroll
   for (int i = 0; i < 128 / kRows; ++i) {
     const int t = qt * 128 + r0 + i * kRows;
     vo[i] = vd[i] = make_uint4(0u, 0u, 0u, 0u);
+    // rows past N: probability 2^-inf
+    lse[i] = -INFINITY;
     if (t < p.N) {
+      if (c == 0) lse[i] = __ldg(p.lse + static_cast<int64_t>(bh) * p.Np + t);
       const int64_t off = bwd_row(p, bh, t, D) * 2 + c * 16;
       vo[i] = ld_global_nc_v4(p.o + off);
       vd[i] = ld_global_nc_v4(p.dout + off);
@@ -127,11 +131,10 @@ __global__ void __launch_bounds__(256) attention_delta_kernel(const __grid_const
     }
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const int r = r0 + i * kRows, t = qt * 128 + r;
+    const int r = r0 + i * kRows;
     if (c == 0) {
-      // rows without a key (lse = -inf) and rows past N: probability 2^-inf
-      const float l = t < p.N ? p.lse[static_cast<int64_t>(bh) * p.Np + t] : -INFINITY;
-      stat[r] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+      // (rows without a key, lse = -inf, too)
+      stat[r] = lse[i] == -INFINITY ? -INFINITY : -lse[i] * 1.4426950408889634f;
       stat[128 + r] = -s;
     }
   }
