@@ -118,13 +118,14 @@ class Cta:
         for j in range(self.T):
             par, ys, nxt = j & 1, j & 1, j + 1 < self.T
             xn, xnp = (0, xp ^ 1) if xs == 2 else (xs + 1, xp)
+            if nxt:
+                yield self.x_full[xn], xnp
             for h in range(2):
                 yield self.p[h], par
                 self.mma([(("P", h), ("P", j)), ("R0", ("S", j)), (("Y", ys), ("Y", j))],
                          add=("A0", (j, h)))
             self.commit(self.y_empty[ys])
             if nxt:
-                yield self.x_full[xn], xnp
                 if self.mistake == "S before dV":
                     self.queue.insert(0, ("mma", [], ("R0", ("S", j + 1)), None))
                 self.scores(0, "X", xn, j + 1, ("S", j + 1), "R0")
