@@ -499,6 +499,34 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^x of two values on the FMA pipe, for x below 128: x = n + r with n the
+// nearest integer (adding 1.5 * 2^23 leaves it in the low bits), 2^r by a
+// polynomial of degree 4 on [-1/2, 1/2], n added to the exponent.  The
+// coefficients minimise the largest relative error under p(0) = 1 (a linear
+// programme over 4,001 Chebyshev points): 2.9e-6 with them rounded to fp32.  At
+// and below -127, -inf included, the result is exactly +0 (n = -127 cancels the
+// exponent of p(0)); NaN gives a huge value that rounds to a bf16 infinity.
+__device__ __forceinline__ void ex2_poly(uint64_t x, uint32_t &lo, uint32_t &hi) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-127.f));
+  x = f2_pack(x0, x1);
+  constexpr float kMagic = 12582912.f;
+  const auto both = [](float c) { return f2_pack(c, c); };
+  const uint64_t t = f2_add(x, both(kMagic));
+  const uint64_t r = f2_fma(f2_add(t, both(-kMagic)), both(-1.f), x);
+  uint64_t y = f2_fma(r, both(0x1.3a1804p-7f), both(0x1.c9fcb2p-5f));
+  y = f2_fma(r, y, both(0x1.ec0326p-3f));
+  y = f2_fma(r, y, both(0x1.62e12cp-1f));
+  y = f2_fma(r, y, both(1.f));
+  float t0, t1, y0, y1;
+  f2_unpack(t, t0, t1);
+  f2_unpack(y, y0, y1);
+  lo = __float_as_uint(y0) + (__float_as_uint(t0) << 23);
+  hi = __float_as_uint(y1) + (__float_as_uint(t1) << 23);
+}
+
 // Two fp32 -> packed E4M3x2 (round to nearest even, saturating to +-448);
 // `lo` in bits 0..7.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
