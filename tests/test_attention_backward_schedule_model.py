@@ -35,13 +35,14 @@ class Bar:
 class Cta:
     """One CTA: shared state, the tensor core's queue and the loads in flight."""
 
-    def __init__(self, T, is_dq, nt, mistake=None):
+    def __init__(self, T, is_dq, nt, tiles, mistake=None):
         self.T, self.is_dq, self.nt, self.mistake = T, is_dq, nt, mistake
+        self.tiles = tiles     # of scores in tensor memory: 1, or 2 with D = 64
         one = lambda n: [Bar() for _ in range(n)]
         self.own, self.x_full, self.x_empty = one(4), one(3), one(3)
         self.y_full, self.y_empty, self.stat, self.stat_empty = one(2), one(2), one(2), one(2)
-        self.s, self.s_free, self.dp, self.acc = Bar(), Bar(2), Bar(), Bar()
-        self.p, self.ds = one(2), one(2)
+        self.s, self.s_free, self.dp, self.acc = one(2), Bar(2), Bar(), Bar()
+        self.p, self.ds = [one(2), one(2)], one(2)
         self.mem = {}          # shared and tensor memory: name -> content
         self.queue = []        # the tensor core, in issue order
         self.loads = []        # (slot, content, barrier)
@@ -102,14 +103,23 @@ class Cta:
             if j == 0 and self.nt == 2:
                 self.load(("own", 2 + own), ("own", 2 + own), self.own[2 + own])
 
+    def tile(self, i):
+        """Item i's score tile: name, barrier index, parity."""
+        b = i % self.tiles
+        return f"R0.{b}", b, (i // self.tiles) & 1
+
+    def next_scores(self, i, own, xn, j):
+        name, b, _ = self.tile(i)
+        self.scores(own, "X", xn, j, ("S", i), name)
+        self.commit(self.s[b])
+
     def scores(self, own, ring, stage, j, tile, out):
         self.mma([(("own", own), ("own", own)), ((ring, stage), (ring, j))], write=(out, tile))
 
     def issue_dkdv(self):
         yield self.own[0], 0
         yield self.x_full[0], 0
-        self.scores(0, "X", 0, 0, ("S", 0), "R0")
-        self.commit(self.s)
+        self.next_scores(0, 0, 0, 0)
         yield self.own[1], 0
         yield self.y_full[0], 0
         self.scores(1, "Y", 0, 0, ("dP", 0), "R1")
@@ -120,16 +130,18 @@ class Cta:
             xn, xnp = (0, xp ^ 1) if xs == 2 else (xs + 1, xp)
             if nxt:
                 yield self.x_full[xn], xnp
+            if nxt and (self.tiles == 2 or self.mistake == "S before dV"):
+                self.next_scores(j + 1, 0, xn, j + 1)
             for h in range(2):
-                yield self.p[h], par
-                self.mma([(("P", h), ("P", j)), ("R0", ("S", j)), (("Y", ys), ("Y", j))],
-                         add=("A0", (j, h)))
+                name, b, sp = self.tile(j)
+                if self.mistake == "one barrier for two tiles":
+                    b, sp = 0, par
+                yield self.p[b][h], sp
+                self.mma([(("P", h, j % self.tiles), ("P", j)), (name, ("S", j)),
+                          (("Y", ys), ("Y", j))], add=("A0", (j, h)))
             self.commit(self.y_empty[ys])
-            if nxt:
-                if self.mistake == "S before dV":
-                    self.queue.insert(0, ("mma", [], ("R0", ("S", j + 1)), None))
-                self.scores(0, "X", xn, j + 1, ("S", j + 1), "R0")
-                self.commit(self.s)
+            if nxt and self.tiles == 1 and self.mistake != "S before dV":
+                self.next_scores(j + 1, 0, xn, j + 1)
             for h in range(2):
                 yield self.ds[h], par
                 self.mma([(("dS", h), ("dS", j)), ("R1", ("dP", j)), (("X", xs), ("X", j))],
@@ -147,8 +159,7 @@ class Cta:
         nt = self.nt
         yield self.own[0], 0
         yield self.x_full[0], 0
-        self.scores(0, "X", 0, 0, ("S", 0), "R0")
-        self.commit(self.s)
+        self.next_scores(0, 0, 0, 0)
         yield self.own[1], 0
         yield self.y_full[0], 0
         self.scores(1, "Y", 0, 0, ("dP", 0), "R1")
@@ -165,10 +176,9 @@ class Cta:
             if nxt:
                 if tn == 0:
                     yield self.x_full[xn], (jn >> 1) & 1
-                if self.mistake != "S without its reader":
+                if self.tiles == 1 and self.mistake != "S without its reader":
                     yield self.s_free, par
-                self.scores(2 * tn, "X", xn, jn, ("S", i + 1), "R0")
-                self.commit(self.s)
+                self.next_scores(i + 1, 2 * tn, xn, jn)
             for h in range(2):
                 yield self.ds[h], par
                 self.mma([(("dS", h), ("dS", i)), ("R1", ("dP", i)), (("X", xs), ("X", j))],
@@ -190,16 +200,17 @@ class Cta:
             par = i & 1
             if not self.is_dq:
                 yield self.stat[par], (i >> 1) & 1
-            yield self.s, par
-            self.expect("R0", ("S", i))
+            name, b, sp = self.tile(i)
+            yield self.s[b], sp
+            self.expect(name, ("S", i))
             yield None                       # (the scores on their way to registers)
-            self.expect("R0", ("S", i))
-            if self.is_dq:
+            self.expect(name, ("S", i))
+            if self.is_dq and self.tiles == 1:
                 self.s_free.arrive()
-            else:
+            if not self.is_dq:
                 self.expect(("stat", par), ("stat", i))
-                self.mem[("P", h)] = ("P", i)
-                self.p[h].arrive()
+                self.mem[("P", h, b)] = ("P", i)
+                self.p[0 if self.mistake == "one barrier for two tiles" else b][h].arrive()
             yield self.dp, par
             self.expect("R1", ("dP", i))
             if not self.is_dq:
@@ -211,8 +222,8 @@ class Cta:
         yield self.acc, 0
 
 
-def simulate(T, is_dq, nt, rng, mistake=None):
-    c = Cta(T, is_dq, nt, mistake)
+def simulate(T, is_dq, nt, tiles, rng, mistake=None):
+    c = Cta(T, is_dq, nt, tiles, mistake)
     roles = [c.producer(True), c.producer(False), c.issue_dq() if is_dq else c.issue_dkdv(),
              c.elementwise(0), c.elementwise(1)]
     waiting = [next(r, "end") for r in roles]
@@ -235,25 +246,28 @@ def simulate(T, is_dq, nt, rng, mistake=None):
         else:
             waiting[i] = next(roles[i], "end")
     assert all(w == "end" for w in waiting), "blocked"
-    tiles = [(j, h) for j in range(T) for h in range(2)]
-    assert c.sums["A0"] == tiles
-    assert c.sums["A1"] == (tiles if not is_dq or nt == 2 else [])
+    every = [(j, h) for j in range(T) for h in range(2)]
+    assert c.sums["A0"] == every
+    assert c.sums["A1"] == (every if not is_dq or nt == 2 else [])
 
 
+@pytest.mark.parametrize("tiles", [1, 2])
 @pytest.mark.parametrize("is_dq,nt", [(False, 1), (True, 1), (True, 2)])
-def test_every_interleaving_ends_with_the_right_operands(is_dq, nt):
+def test_every_interleaving_ends_with_the_right_operands(is_dq, nt, tiles):
     for T in (1, 2, 3, 4, 5, 8, 13):
         for seed in range(60):
-            simulate(T, is_dq, nt, random.Random(1000 * T + seed))
+            simulate(T, is_dq, nt, tiles, random.Random(1000 * T + seed))
 
 
-@pytest.mark.parametrize("is_dq,nt,mistake", [
-    (False, 1, "statistics wait on dS"), (False, 1, "S before dV"), (True, 2, "S without its reader")])
-def test_planted_mistakes_are_found(is_dq, nt, mistake):
+@pytest.mark.parametrize("is_dq,nt,tiles,mistake", [
+    (False, 1, 1, "statistics wait on dS"), (False, 1, 2, "statistics wait on dS"),
+    (False, 1, 1, "S before dV"), (True, 2, 1, "S without its reader"),
+    (False, 1, 2, "one barrier for two tiles")])
+def test_planted_mistakes_are_found(is_dq, nt, tiles, mistake):
     failed = 0
     for seed in range(300):
         try:
-            simulate(9, is_dq, nt, random.Random(seed), mistake)
+            simulate(9, is_dq, nt, tiles, random.Random(seed), mistake)
         except AssertionError:
             failed += 1
     assert failed > 0, mistake
