@@ -19,7 +19,8 @@
 // at 1.28 PFLOP/s, cuBLAS holds 1.38 there).  A 128 x 128 tile takes 2,700 cycles
 // in a dK/dV CTA (its four products 2,048) and 2,050 in a dQ CTA (1,536); a
 // polynomial for part of the exponentials brought that to 2,450 and 1,970, and
-// the time, at the cap, not at all.  Short problems are bound by a CTA's chain.
+// the time, at the cap, not at all (D = 64 has one, see below).  Short problems
+// are bound by a CTA's chain.
 //
 // One launch holds both kinds of CTA:
 //   dK, dV: 128 keys; walks the 128-query tiles.  Scores are computed
@@ -165,8 +166,8 @@ struct AttnBwdCfg {
   static constexpr uint32_t kColA1 = 256 + D;         // dK, or dQ of tile 1
   static constexpr uint32_t kTmemCols = 512;
   // With D = 64 tensor memory holds a second tile of scores, so that S_{j+1}
-  // need not wait for the tile before it: 8,192 tokens x 20 heads 1.32 instead of
-  // 1.34 ms.
+  // need not wait for the tile before it: 32,760 tokens x 12 heads 12.3 instead of
+  // 12.9 ms, 1,024 x 4 heads 17.6 instead of 18.8 us.
   static constexpr int kScores = D == 64 ? 2 : 1;
   static constexpr uint32_t kColS1 = 384;
 };
@@ -545,10 +546,10 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
     };
     // pr = 2^(pr * scale * log2(e) + bias pair), 32 columns.  With D = 64 the
     // products take half as long and the special-function unit bounds a tile,
-    // so six of sixteen pairs go to the FMA pipe (8,192 tokens x 20 heads: 1.34
-    // instead of 1.43 ms; four 1.39, eight 1.36).  With D = 128 that cost 1 to 2 %
-    // at the power cap.
-    constexpr int kPolyPairs = D == 64 ? 6 : 0;
+    // so four of sixteen pairs go to the FMA pipe (32,760 tokens x 12 heads: 12.25
+    // instead of 12.55 ms, 1,024 x 4 heads 17.8 instead of 19.2 us; six the same,
+    // eight 12.8 ms).  With D = 128 it cost 1 to 2 % at the power cap.
+    constexpr int kPolyPairs = D == 64 ? 4 : 0;
     auto exps = [&](uint32_t *pr, auto bias) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
