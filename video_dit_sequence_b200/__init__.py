@@ -298,20 +298,21 @@ def _same_device(*tensors):
     return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _operands(device, *specs):
-    """Addresses of (tensor, shape, name, dtype) operands, all on `device`."""
-    torch = _torch()
-    Tensor, out = torch.Tensor, []
-    for t, shape, name, dtype in specs:
-        if t is None:
-            out.append(None)
-        elif (isinstance(t, Tensor) and t.device == device and t.dtype == dtype and
-              t.shape == shape and t.is_contiguous()):
-            out.append(t.data_ptr())
-        else:
-            out.append(_ptr(t, shape, name, dtype))
-            if t.device != device:
-                raise ValueError(f"operands on several devices: {t.device}, {device}")
+def _operands(device, *groups):
+    """Addresses of operands, all on `device`: groups of (elements, dtype,
+    shape, (tensor, name), ...)."""
+    Tensor, index, out = _torch().Tensor, device.index, []
+    for n, dtype, shape, *tensors in groups:
+        for t, name in tensors:
+            if t is None:
+                out.append(None)
+            elif (isinstance(t, Tensor) and t.get_device() == index and t.dtype is dtype and
+                  t.numel() == n and t.is_contiguous()):
+                out.append(t.data_ptr())
+            else:
+                out.append(_ptr(t, shape, name, dtype))
+                if t.device != device:
+                    raise ValueError(f"operands on several devices: {t.device}, {device}")
     return out
 
 
@@ -325,7 +326,7 @@ def _device_of(t, name):
 def _call(fn, where, device, *args):
     """Runs a library call with `device` current."""
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         status = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -642,13 +643,14 @@ def _attention_backward(name, ts, q, k, v, o, lse, do, dq, dk, dv, shape, worksp
         if t is None:
             raise TypeError(f"{n} must be a CUDA tensor")
     need = attention_backward_workspace(shape)   # (refuses a shape out of range)
-    ops = _operands(dev, (q, ts, "q", bf16), (k, ts, "k", bf16), (v, ts, "v", bf16),
-                    (o, ts, "o", bf16), (lse, shape.lse_shape, "lse", torch.float32),
-                    (do, ts, "do", bf16), (dq, ts, "dq", bf16), (dk, ts, "dk", bf16),
-                    (dv, ts, "dv", bf16))
+    n, ls = math.prod(ts), shape.lse_shape
+    a = _operands(dev, (n, bf16, ts, (q, "q"), (k, "k"), (v, "v"), (o, "o"), (do, "do"),
+                        (dq, "dq"), (dk, "dk"), (dv, "dv")),
+                  (math.prod(ls), torch.float32, ls, (lse, "lse")))
     st = _stream(stream, dev)
     ws = _workspace(workspace, need, dev, stream)
-    _call(getattr(load(), name), name, dev, *ops, ws.data_ptr(), ctypes.byref(shape.c()), st)
+    _call(getattr(load(), name), name, dev, a[0], a[1], a[2], a[3], a[8], a[4], a[5], a[6], a[7],
+          ws.data_ptr(), ctypes.byref(shape.c()), st)
 
 
 def attention_backward(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None, stream=None):
@@ -693,22 +695,27 @@ def _workspace(workspace, nbytes, device, stream):
 
 def _norm_params(params, shape: Shape, hidden: int):
     """(param_layout, param_type, torch dtype, tensor shape) of layer norm's
-    parameters; the given ones must agree."""
+    parameters, which must agree."""
     torch = _torch()
-    given = [t for t in params if t is not None]
-    if not given:
+    first = None
+    for t in params:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("layer norm parameters must be tensors")
+        if first is None:
+            first, dtype = t, t.dtype
+            fp32 = dtype is torch.float32
+            if not fp32 and dtype is not torch.bfloat16:
+                raise TypeError(f"layer norm parameters must be bfloat16 or float32, got {dtype}")
+            per_sample = t.dim() == 2
+            pshape = (shape.B, hidden) if per_sample else (hidden,)
+        if t.dtype is not dtype or t.shape != pshape:
+            raise ValueError(f"layer norm parameters must all be {dtype} of shape ({hidden},) or "
+                             f"({shape.B}, {hidden}), got {t.dtype} {tuple(t.shape)}")
+    if first is None:
         return 0, 0, torch.bfloat16, (hidden,)
-    t = given[0]
-    if not all(isinstance(o, torch.Tensor) for o in given):
-        raise TypeError("layer norm parameters must be tensors")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"layer norm parameters must be bfloat16 or float32, got {t.dtype}")
-    pshape = (hidden,) if t.dim() == 1 else (shape.B, hidden)
-    for o in given:
-        if o.dtype != t.dtype or o.shape != pshape:
-            raise ValueError(f"layer norm parameters must all be {t.dtype} of shape ({hidden},) or "
-                             f"({shape.B}, {hidden}), got {o.dtype} {tuple(o.shape)}")
-    return int(t.dim() == 2), int(t.dtype == torch.float32), t.dtype, pshape
+    return int(per_sample), int(fp32), dtype, pshape
 
 
 def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: float = 1e-6,
@@ -724,11 +731,13 @@ def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: floa
     bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
     full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, bias), shape, hidden)
-    ops = _operands(dev, (x, full, "x", bf16), (weight, pshape, "weight", dtype),
-                    (bias, pshape, "bias", dtype), (y, full, "y", bf16), (mean, rows, "mean", f32),
-                    (rstd, rows, "rstd", f32))
-    _call(load().sp_layer_norm, "sp_layer_norm", dev, *ops, hidden, float(eps), layout, ptype,
-          ctypes.byref(shape.c()), _stream(stream, dev))
+    nrows = math.prod(rows)
+    xp, yp, w, b, m, r = _operands(
+        dev, (nrows * hidden, bf16, full, (x, "x"), (y, "y")),
+        (math.prod(pshape), dtype, pshape, (weight, "weight"), (bias, "bias")),
+        (nrows, f32, rows, (mean, "mean"), (rstd, "rstd")))
+    _call(load().sp_layer_norm, "sp_layer_norm", dev, xp, w, b, yp, m, r, hidden, float(eps), layout,
+          ptype, ctypes.byref(shape.c()), _stream(stream, dev))
 
 
 @functools.lru_cache(maxsize=256)
@@ -754,15 +763,17 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=Non
     bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
     full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, dweight, dbias), shape, hidden)
-    ops = _operands(dev, (dy, full, "dy", bf16), (x, full, "x", bf16),
-                    (weight, pshape, "weight", dtype), (mean, rows, "mean", f32),
-                    (rstd, rows, "rstd", f32), (dx, full, "dx", bf16),
-                    (dweight, pshape, "dweight", dtype), (dbias, pshape, "dbias", dtype))
+    nrows = math.prod(rows)
+    dyp, xp, dxp, w, dw, db, m, r = _operands(
+        dev, (nrows * hidden, bf16, full, (dy, "dy"), (x, "x"), (dx, "dx")),
+        (math.prod(pshape), dtype, pshape, (weight, "weight"), (dweight, "dweight"),
+         (dbias, "dbias")),
+        (nrows, f32, rows, (mean, "mean"), (rstd, "rstd")))
     st = _stream(stream, dev)
     ws = None
     if dweight is not None or dbias is not None:
         ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden), dev, stream)
-    _call(load().sp_layer_norm_backward, "sp_layer_norm_backward", dev, *ops,
+    _call(load().sp_layer_norm_backward, "sp_layer_norm_backward", dev, dyp, xp, w, m, r, dxp, dw, db,
           None if ws is None else ws.data_ptr(), hidden, layout, ptype, ctypes.byref(shape.c()), st)
 
 
