@@ -298,22 +298,27 @@ def _same_device(*tensors):
     return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _operands(device, *groups):
-    """Addresses of operands, all on `device`: groups of (elements, dtype,
-    shape, (tensor, name), ...)."""
-    Tensor, index, out = _torch().Tensor, device.index, []
-    for n, dtype, shape, *tensors in groups:
-        for t, name in tensors:
+def _operands(device, names, tensors, dtypes, sizes, shapes):
+    """Addresses of operands, all on `device`, of these types and sizes."""
+    index, out = device.index, []
+    try:
+        for t, dtype, n in zip(tensors, dtypes, sizes):
             if t is None:
                 out.append(None)
-            elif (isinstance(t, Tensor) and t.get_device() == index and t.dtype is dtype and
-                  t.numel() == n and t.is_contiguous()):
+            elif (t.get_device() == index and t.dtype is dtype and t.numel() == n and
+                  t.is_contiguous()):
                 out.append(t.data_ptr())
             else:
-                out.append(_ptr(t, shape, name, dtype))
-                if t.device != device:
-                    raise ValueError(f"operands on several devices: {t.device}, {device}")
-    return out
+                break
+        else:
+            return out
+    except AttributeError:   # not a tensor
+        pass
+    for t, dtype, shape, name in zip(tensors, dtypes, shapes, names):   # which one, and why
+        _ptr(t, shape, name, dtype)
+        if t is not None and t.device != device:
+            raise ValueError(f"operands on several devices: {t.device}, {device}")
+    raise ValueError("operands could not be used")
 
 
 def _device_of(t, name):
@@ -643,14 +648,14 @@ def _attention_backward(name, ts, q, k, v, o, lse, do, dq, dk, dv, shape, worksp
         if t is None:
             raise TypeError(f"{n} must be a CUDA tensor")
     need = attention_backward_workspace(shape)   # (refuses a shape out of range)
-    n, ls = math.prod(ts), shape.lse_shape
-    a = _operands(dev, (n, bf16, ts, (q, "q"), (k, "k"), (v, "v"), (o, "o"), (do, "do"),
-                        (dq, "dq"), (dk, "dk"), (dv, "dv")),
-                  (math.prod(ls), torch.float32, ls, (lse, "lse")))
+    n, ls, nl = math.prod(ts), shape.lse_shape, math.prod(shape.lse_shape)
+    ops = _operands(dev, ("q", "k", "v", "o", "lse", "do", "dq", "dk", "dv"),
+                    (q, k, v, o, lse, do, dq, dk, dv),
+                    (bf16, bf16, bf16, bf16, torch.float32, bf16, bf16, bf16, bf16),
+                    (n, n, n, n, nl, n, n, n, n), (ts, ts, ts, ts, ls, ts, ts, ts, ts))
     st = _stream(stream, dev)
     ws = _workspace(workspace, need, dev, stream)
-    _call(getattr(load(), name), name, dev, a[0], a[1], a[2], a[3], a[8], a[4], a[5], a[6], a[7],
-          ws.data_ptr(), ctypes.byref(shape.c()), st)
+    _call(getattr(load(), name), name, dev, *ops, ws.data_ptr(), ctypes.byref(shape.c()), st)
 
 
 def attention_backward(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None, stream=None):
@@ -731,13 +736,13 @@ def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: floa
     bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
     full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, bias), shape, hidden)
-    nrows = math.prod(rows)
-    xp, yp, w, b, m, r = _operands(
-        dev, (nrows * hidden, bf16, full, (x, "x"), (y, "y")),
-        (math.prod(pshape), dtype, pshape, (weight, "weight"), (bias, "bias")),
-        (nrows, f32, rows, (mean, "mean"), (rstd, "rstd")))
-    _call(load().sp_layer_norm, "sp_layer_norm", dev, xp, w, b, yp, m, r, hidden, float(eps), layout,
-          ptype, ctypes.byref(shape.c()), _stream(stream, dev))
+    n = math.prod(rows)
+    nx, nw = n * hidden, math.prod(pshape)
+    ops = _operands(dev, ("x", "weight", "bias", "y", "mean", "rstd"),
+                    (x, weight, bias, y, mean, rstd), (bf16, dtype, dtype, bf16, f32, f32),
+                    (nx, nw, nw, nx, n, n), (full, pshape, pshape, full, rows, rows))
+    _call(load().sp_layer_norm, "sp_layer_norm", dev, *ops, hidden, float(eps), layout, ptype,
+          ctypes.byref(shape.c()), _stream(stream, dev))
 
 
 @functools.lru_cache(maxsize=256)
@@ -763,17 +768,18 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=Non
     bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
     full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, dweight, dbias), shape, hidden)
-    nrows = math.prod(rows)
-    dyp, xp, dxp, w, dw, db, m, r = _operands(
-        dev, (nrows * hidden, bf16, full, (dy, "dy"), (x, "x"), (dx, "dx")),
-        (math.prod(pshape), dtype, pshape, (weight, "weight"), (dweight, "dweight"),
-         (dbias, "dbias")),
-        (nrows, f32, rows, (mean, "mean"), (rstd, "rstd")))
+    n = math.prod(rows)
+    nx, nw = n * hidden, math.prod(pshape)
+    ops = _operands(dev, ("dy", "x", "weight", "mean", "rstd", "dx", "dweight", "dbias"),
+                    (dy, x, weight, mean, rstd, dx, dweight, dbias),
+                    (bf16, bf16, dtype, f32, f32, bf16, dtype, dtype),
+                    (nx, nx, nw, n, n, nx, nw, nw),
+                    (full, full, pshape, rows, rows, full, pshape, pshape))
     st = _stream(stream, dev)
     ws = None
     if dweight is not None or dbias is not None:
         ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden), dev, stream)
-    _call(load().sp_layer_norm_backward, "sp_layer_norm_backward", dev, dyp, xp, w, m, r, dxp, dw, db,
+    _call(load().sp_layer_norm_backward, "sp_layer_norm_backward", dev, *ops,
           None if ws is None else ws.data_ptr(), hidden, layout, ptype, ctypes.byref(shape.c()), st)
 
 
