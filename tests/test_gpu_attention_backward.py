@@ -170,6 +170,35 @@ def test_rows_without_a_key_and_negative_statistics():
     assert (dq[:, 7] == 0).all() and (dq[:, 290:, 1] == 0).all()
 
 
+@pytest.mark.parametrize("layout,D,P", [("seq", 128, 3), ("seq", 64, 1), ("head", 64, 2), ("head", 128, 2)])
+def test_values_that_are_not_finite_stay_in_their_head(layout, D, P):
+    """A NaN in one query reaches that query's gradient and, through its row of
+    probabilities, every dK and dV of the head, and nothing else; one in a row of
+    dO likewise.  The other heads repeat bit for bit."""
+    B, N, H = 2, 333, 2
+    scale = 1 / math.sqrt(D)
+    shape = sp.Shape(B, N, H, D, P)
+    clean = _inputs(B, N, H, D, seed=21)
+    o, lse = _forward64(*clean[:3], scale)
+    base = _call(layout, shape, *clean[:3], o, lse, clean[3])
+    base = [_from_layout(t, layout, B, N, H, D, P)[0] for t in base]
+    for which in (0, 3):    # q, dO
+        for row in (5, 18, 200):
+            t = [x.clone() for x in clean]
+            t[which][1, row, 1, :] = float("nan")
+            o, lse = _forward64(*t[:3], scale)
+            d = _call(layout, shape, *t[:3], o, lse, t[3])
+            dq, dk, dv = (_from_layout(x, layout, B, N, H, D, P)[0] for x in d)
+            assert not torch.isfinite(dq[1, row, 1]).any()
+            rest = torch.ones(B, N, H, dtype=torch.bool, device="cuda")
+            rest[1, row, 1] = False
+            assert torch.equal(dq[rest], base[0][rest])
+            assert not torch.isfinite(dk[1, :, 1]).any() and not torch.isfinite(dv[1, :, 1]).any()
+            for got, want in ((dk, base[1]), (dv, base[2])):
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1, :, 0], want[1, :, 0])
+    assert sp.device_status() == sp.SP_OK
+
+
 @pytest.mark.parametrize("B,N,H", [(1, 1025, 4), (2, 2200, 12)])
 def test_results_repeat_and_depend_on_neither_degree_nor_layout(B, N, H):
     D = 128
