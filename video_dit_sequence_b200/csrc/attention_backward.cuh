@@ -677,33 +677,45 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
     }
     // epilogue: warpgroup h stores accumulator h (dV and dK, or dQ of query
-    // tile h), a row per thread
+    // tile h).  A thread has a row; through shared memory (the own tiles, which
+    // the last MMA has read; chunks swizzled as there) a warp's stores cover
+    // whole rows instead of 16 bytes of each of 32 (4,096 tokens x 40 heads 996
+    // instead of 1,046 us, 1,024 x 18 heads 48 instead of 53).
     if (ok) ok = wait(bar_acc, 0);
-    if (ok) {
+    if (ok && (!is_dq || h < nt)) {
       tc_fence_after();
       const int tok = is_dq ? t0 + 128 * h + row : t0 + row;
       const float f = !is_dq && h == 0 ? 1.0f : p.scale;
       __nv_bfloat16 *base = is_dq ? p.dq : h == 0 ? p.dv : p.dk;
-      const bool valid = tok < p.N && (!is_dq || h < nt);
-      __nv_bfloat16 *dst = base + bwd_row(p, bh, valid ? tok : 0, D);
+      const uint64_t dst =
+          tok < p.N ? reinterpret_cast<uint64_t>(base + bwd_row(p, bh, tok, D)) : 0;
       const uint32_t tA = tmem + lane_bits + (h == 0 ? C::kColA0 : C::kColA1);
+      const uint32_t stage = sbase + C::kOffOwn + warp * (64 * D);
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tmem_ld32(tA + c, o);
         tmem_wait_ld();
-        if (valid) {
-          uint4 *d4 = reinterpret_cast<uint4 *>(dst + c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * f,
-                                 __uint_as_float(o[8 * i + 2 * e + 1]) * f);
-            d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * f,
+                               __uint_as_float(o[8 * i + 2 * e + 1]) * f);
+          st_shared_v4(stage + lane * 2 * D + (((c / 8 + i) ^ (lane & 7)) << 4),
+                       make_uint4(w[0], w[1], w[2], w[3]));
         }
+      }
+      __syncwarp();
+      constexpr int kChunks = D / 8;
+      const int cc = lane % kChunks;
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 32 / kChunks) {
+        const int r = r0 + lane / kChunks;
+        const uint64_t d = __shfl_sync(0xffffffffu, dst, r);
+        if (d != 0)
+          reinterpret_cast<uint4 *>(d)[cc] = ld_shared_v4(stage + r * 2 * D + ((cc ^ (r & 7)) << 4));
       }
     }
   }
