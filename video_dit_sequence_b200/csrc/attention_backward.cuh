@@ -172,9 +172,10 @@ struct AttnBwdCfg {
   static constexpr uint32_t kColS1 = 384;
 };
 
-// Blocks of a head: its dQ pairs of query tiles first (they run longest), then
-// its key tiles; the CTAs that run together belong to one or two heads, whose
-// Q, K, V and dO stay in L2.
+// Blocks: every head's pairs of query tiles first, since they run longest, then
+// every head's key tiles (2,048 tokens x 12 heads 78 us; head by head 92.5,
+// and the same within 1 % from 4,096 tokens on).  The CTAs that run together
+// belong to one or two heads, whose Q, K, V and dO stay in L2.
 template <int D>
 __global__ void __launch_bounds__(384, 1)
 attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -244,9 +245,11 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
   const uint32_t tmem = *tmem_slot;
 
   const int T2 = (T + p.dq_tiles - 1) / p.dq_tiles;
-  const int bh = blockIdx.x / (T + T2), item = blockIdx.x - bh * (T + T2);
-  const bool is_dq = item < T2;
-  const int t0 = is_dq ? item * p.dq_tiles * 128 : (item - T2) * 128;  // first own token
+  const int n_dq = p.BH * T2, blk = blockIdx.x;
+  const bool is_dq = blk < n_dq;
+  const int i_kind = is_dq ? blk : blk - n_dq, per = is_dq ? T2 : T;
+  const int bh = i_kind / per;
+  const int t0 = (i_kind - bh * per) * (is_dq ? p.dq_tiles * 128 : 128);  // first own token
   const int nt = is_dq && p.dq_tiles == 2 && t0 + 128 < p.N ? 2 : 1;
   const int b = bh / p.H, hg = bh - b * p.H;
 
