@@ -13,7 +13,7 @@
 // moves 64 KB out of every SM per tile; it took 18.5 ms at 480p (12 heads,
 // 32,760 tokens) and 1.52 ms at 4,096 tokens x 40 heads.  Here scores and dP are
 // computed twice instead, seven products, and every sum stays in tensor memory:
-// 18.0 and 1.06 ms.  Results repeat bit for bit and depend neither on timing nor
+// 17.9 and 1.00 ms.  Results repeat bit for bit and depend neither on timing nor
 // on P.
 // What bounds it: at 480p the 1,000 W power cap (1.5 GHz of 1.97; seven products
 // at 1.28 PFLOP/s, cuBLAS holds 1.38 there).  A 128 x 128 tile takes 2,700 cycles
@@ -28,8 +28,8 @@
 //           bf16 for the tensor core as the forward pass rounds P, are the A
 //           operands of dV += P^T dO and dK += dS^T Q from tensor memory.
 //   dQ:     two tiles of 128 queries, which take turns at each 128-key tile
-//           (one K, V load serves both), or one when that still leaves SMs
-//           free; dS is the A operand of dQ += dS K.
+//           (one K, V load serves both), or one tile (the launcher has the
+//           rule); dS is the A operand of dQ += dS K.
 // Roles (12 warps):
 //   warps 0-7   elementwise: warpgroup h takes columns 64h .. 64h+63 of a tile,
 //               one thread per row (key, or query for dQ)

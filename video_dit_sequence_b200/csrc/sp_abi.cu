@@ -988,11 +988,16 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
   p.hsplit = Hx;
   p.T = (N + 127) / 128;
   p.BH = B * H;
-  // dQ CTAs of one query tile while all CTAs fit the 148 SMs at once (1,024
-  // tokens x 4 heads of 64: 21 instead of 25 us, x 9 heads of 128: 29 instead of
-  // 35 us); of two otherwise, which halves their loads (x 10 heads: 35 instead
-  // of 42 us, 4,096 tokens x 40 heads: 1.06 instead of 1.17 ms).
-  p.dq_tiles = static_cast<int64_t>(p.BH) * 2 * p.T <= 148 ? 1 : 2;
+  // dQ CTAs of two query tiles halve their loads, those of one tile end sooner:
+  // one tile where that takes no more rounds of CTAs on the 148 SMs (1,024 tokens
+  // of 128 columns: x 9 heads, one round, 25 instead of 29 us; x 18 heads, two, 39
+  // instead of 41; x 10 heads, two instead of one, 37 instead of 29; 4,096 x 10
+  // heads, five instead of four, 293 instead of 262).  From 296 tiles on it
+  // always takes more.
+  const auto rounds = [&p](int tiles) {
+    return (static_cast<int64_t>(p.BH) * (p.T + (p.T + tiles - 1) / tiles) + 147) / 148;
+  };
+  p.dq_tiles = rounds(1) <= rounds(2) ? 1 : 2;
   p.nl_split = rank_major ? Nl : 0;
   p.scale = s->scale > 0.f ? s->scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.scale_log2e = p.scale * 1.4426950408889634f;
