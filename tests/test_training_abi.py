@@ -108,3 +108,10 @@ def test_attention_backward_workspace(lib):
         assert n == sp.attention_backward_workspace(sp.Shape(B, N, H, D, 5))
     with pytest.raises(sp.SpError):
         sp.attention_backward_workspace(sp.Shape(1, 10, 1, 32, 1))
+
+
+def test_backward_step_needs_a_step():
+    torch = pytest.importorskip("torch")
+    rank = sp.UlyssesRank(sp.Shape(1, 10, 2, 64, 2))
+    with pytest.raises(RuntimeError, match="there was none"):
+        rank.backward_step(torch.zeros(1), None, lambda send, recv: None)

@@ -558,6 +558,8 @@ class UlyssesRank:
     def backward_step(self, do, lse, all_to_all):
         """The way back of the last step, which was given this lse: returns the
         gradients of its q, k and v shards (this object's buffers)."""
+        if "o" not in self._bufs:
+            raise RuntimeError("backward_step goes back over a step: there was none")
         q, k, v = self.recv_buffers(do)
         recv = self._buf("recv_do", self.shape.send_chunks, do)
         all_to_all(self.send_grad(do), recv)
