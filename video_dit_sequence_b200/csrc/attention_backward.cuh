@@ -68,6 +68,12 @@ struct AttnBwdParams {
   int32_t *status;
 };
 
+// Tensor maps of Q, K, V and dO with boxes of 128 rows and, for rank-major
+// shards, of 32 and of 8.
+struct AttnBwdMaps {
+  CUtensorMap tile[4], quad[4], group[4];
+};
+
 // Element offset of token `t` of head bh's row in q, k, v, o and their gradients.
 __device__ __forceinline__ int64_t bwd_row(const AttnBwdParams &p, int bh, int t, int D) {
   const int b = bh / p.H, hg = bh - b * p.H;
@@ -178,10 +184,7 @@ struct AttnBwdCfg {
 // belong to one or two heads, whose Q, K, V and dO stay in L2.
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
-                          const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV,
-                          const __grid_constant__ CUtensorMap tmDO,
+attention_backward_kernel(const __grid_constant__ AttnBwdMaps maps,
                           const __grid_constant__ AttnBwdParams p) {
   using C = AttnBwdCfg<D>;
   // The swizzled tiles want 1,024-byte alignment, which the dynamic shared
@@ -274,60 +277,74 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int map_head = hg - hs * p.hsplit, map_batch = hs * p.B + b;
       const uint64_t pol_own = policy_evict_first(), pol_ring = policy_evict_last();
       const int nl = p.nl_split;
-      if (lane == 0) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-        prefetch_tmap(&tmDO);
-      }
+      if (lane < 4) prefetch_tmap(&maps.tile[lane]);
       // Rank-major layout: a tile that crosses a shard boundary, or holds
-      // padding slots of the last shard, is copied row by row.
+      // padding slots of the last shard, is loaded in pieces.
       auto tma_ok = [&](int tok) {
         if (nl == 0) return true;
         const int r0 = tok / nl;
         return tok - r0 * nl + 128 <= nl && tok + 128 <= p.N;
       };
-      // 16-byte chunk cc of row r at chunk cc ^ (r mod 8) of its column block,
-      // as the TMA writes it.  Asynchronous copies keep the whole tile in
-      // flight; with loads through registers, four at a time, a tile took
-      // 6 us (777 tokens in 3 shards, 2 x 6 heads: 220 instead of 44 us).
-      auto copy_tile = [&](const uint8_t *base, uint32_t dst, int tok) {
-        constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+      // Lane g has group g, eight rows, 1,024 bytes of each column block as the
+      // TMA swizzles it.  Four groups, or one, that lie within a shard or past N
+      // (zeros, from a box past the shard) are one more TMA load a column block;
+      // the few others are copied row by row, 16-byte chunk cc of row r to chunk
+      // cc ^ (r mod 8).  With all rows copied so a tile took 3 us (2,050 tokens in
+      // 8 shards, 2 x 8 heads: 160 us), and through registers, four loads in
+      // flight, 6; single rows by TMA were slower than copies (150 us).
+      auto load_pieces = [&](int which, const uint8_t *base, uint32_t dst, uint32_t bar, int tok,
+                             uint64_t pol) {
+        auto whole = [&](int n, int rows) {
+          return nl >= rows && (n >= p.N || (n % nl + rows <= nl && n + rows <= p.N));
+        };
+        const int n0 = tok + 8 * lane;
+        const bool quad = lane < 16 && whole(tok + 32 * (lane >> 2), 32);
+        const bool tma = quad || (lane < 16 && whole(n0, 8));
+        const uint32_t by_tma = __ballot_sync(0xffffffffu, tma);
+        if (lane == 0) mbar_expect_tx(bar, __popc(by_tma) * 1024 * C::kHalves);
+        __syncwarp();
+        if (quad ? (lane & 3) == 0 : tma) {
+          const CUtensorMap *m = quad ? &maps.quad[which] : &maps.group[which];
+          const int rk = n0 >= p.N ? 0 : n0 / nl, loc = n0 >= p.N ? nl : n0 - rk * nl;
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_load_5d(dst + h * C::kBlockBytes + lane * 1024, m, bar, h * 64, map_head, loc, b, rk,
+                        pol);
+        }
+        __syncwarp();
+        constexpr int kChunks = D / 8;
         const int cc = lane % kChunks;
         const uint32_t col = dst + (cc >> 3) * C::kBlockBytes;
-        int n = tok + lane / kChunks;                  // token, then its local row
-        const int rk = n / nl;
-        n -= rk * nl;
-        const uint8_t *src = base + cc * 16 +
-                             2 * (rk * p.rank_el + b * p.batch_el + n * p.row_el +
-                                  static_cast<int64_t>(map_head) * D);
-        const int64_t step = 2 * kStep * p.row_el, wrap = 2 * (p.rank_el - nl * p.row_el);
-#pragma unroll 4
-        for (int r = lane / kChunks; r < 128; r += kStep) {
-          const bool in = tok + r < p.N;
-          cp_async16(col + r * 128 + (((cc & 7) ^ (r & 7)) << 4), in ? src : base, in ? 16 : 0);
-          src += step;
-          for (n += kStep; n >= nl; n -= nl) src += wrap;
+        for (uint32_t rest = ~by_tma & 0xffffu; rest != 0; rest &= rest - 1) {
+          const int g8 = 8 * (__ffs(rest) - 1);
+#pragma unroll
+          for (int i = lane / kChunks; i < 8; i += 32 / kChunks) {
+            const int n = tok + g8 + i, rk = n / nl;
+            const bool in = n < p.N;
+            const uint8_t *src = base + cc * 16 +
+                                 2 * (rk * p.rank_el + b * p.batch_el + (n - rk * nl) * p.row_el +
+                                      static_cast<int64_t>(map_head) * D);
+            cp_async16(col + (g8 + i) * 128 + (((cc & 7) ^ i) << 4), in ? src : base, in ? 16 : 0);
+          }
         }
         cp_async_wait();
         fence_proxy_async_smem();
-      };
-      auto load = [&](const CUtensorMap *m, const uint8_t *base, uint32_t dst, uint32_t bar, int tok,
-                      uint64_t pol) {
-        const bool tma = tma_ok(tok);
-        if (!tma) copy_tile(base, dst, tok);
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, tma ? C::kTileBytes : 0);
-          if (tma) {
-            for (int h = 0; h < C::kHalves; ++h) {
-              if (nl == 0) {
-                tma_load_4d(dst + h * C::kBlockBytes, m, bar, h * 64, map_head, tok, map_batch, pol);
-              } else {
-                const int r0 = tok / nl;
-                tma_load_5d(dst + h * C::kBlockBytes, m, bar, h * 64, map_head, tok - r0 * nl, b, r0,
-                            pol);
-              }
+        if (lane == 0) mbar_arrive(bar);
+      };
+      auto load = [&](int which, const uint8_t *base, uint32_t dst, uint32_t bar, int tok,
+                      uint64_t pol) {
+        if (!tma_ok(tok)) {
+          load_pieces(which, base, dst, bar, tok, pol);
+        } else if (lane == 0) {
+          const CUtensorMap *m = &maps.tile[which];
+          mbar_arrive_expect_tx(bar, C::kTileBytes);
+          for (int h = 0; h < C::kHalves; ++h) {
+            if (nl == 0) {
+              tma_load_4d(dst + h * C::kBlockBytes, m, bar, h * 64, map_head, tok, map_batch, pol);
+            } else {
+              const int r0 = tok / nl;
+              tma_load_5d(dst + h * C::kBlockBytes, m, bar, h * 64, map_head, tok - r0 * nl, b, r0,
+                          pol);
             }
           }
         }
@@ -337,8 +354,9 @@ attention_backward_kernel(const __grid_constant__ CUtensorMap tmQ,
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs)) != 0;
       };
       const bool first = warp == 8;
-      const CUtensorMap *mO = first ? (is_dq ? &tmQ : &tmK) : (is_dq ? &tmDO : &tmV);    // own
-      const CUtensorMap *mR = first ? (is_dq ? &tmK : &tmQ) : (is_dq ? &tmV : &tmDO);    // ring
+      // 0 .. 3: Q, K, V, dO
+      const int mO = first ? (is_dq ? 0 : 1) : (is_dq ? 3 : 2);    // own
+      const int mR = first ? (is_dq ? 1 : 0) : (is_dq ? 2 : 3);    // ring
       const uint8_t *gO = first ? (is_dq ? p.q : p.k) : (is_dq ? p.dout : p.v);
       const uint8_t *gR = first ? (is_dq ? p.k : p.q) : (is_dq ? p.v : p.dout);
       const uint32_t ring = sbase + (first ? (is_dq ? C::kOffK2 : C::kOffX)

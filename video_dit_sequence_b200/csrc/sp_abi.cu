@@ -932,7 +932,7 @@ int64_t backward_workspace(const sp_shape *s) {
 }
 
 template <int D>
-sp_status launch_attention_backward(const CUtensorMap *m, const sp::AttnBwdParams &p,
+sp_status launch_attention_backward(const sp::AttnBwdMaps &m, const sp::AttnBwdParams &p,
                                     cudaStream_t cs) {
   using C = sp::AttnBwdCfg<D>;
   static bool attr_set[kMaxDevices] = {};
@@ -946,8 +946,7 @@ sp_status launch_attention_backward(const CUtensorMap *m, const sp::AttnBwdParam
   const unsigned ctas =
       static_cast<unsigned>(p.BH) * (p.T + (p.T + p.dq_tiles - 1) / p.dq_tiles);
   return launch_status(launch_dependent(sp::attention_backward_kernel<D>, dim3(ctas),
-                                        dim3(C::kThreads), C::kSmemBytes, cs, m[0], m[1], m[2],
-                                        m[3], p));
+                                        dim3(C::kThreads), C::kSmemBytes, cs, m, p));
 }
 
 sp_status attention_backward(const void *q, const void *k, const void *v, const void *o,
@@ -973,11 +972,13 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
   const int64_t batch_el = static_cast<int64_t>(seqsharded ? Nl : Np) * Hx * D;
   int32_t *status = status_ptr();
   if (status == nullptr) return SP_ERR_CUDA;
-  CUtensorMap m[4];
+  sp::AttnBwdMaps m;
   const void *src[4] = {q, k, v, d_o};
   for (int i = 0; i < 4; ++i)
-    if (!(rank_major ? make_map5(&m[i], src[i], D, H, Nl, B, P)
-                     : make_map(&m[i], src[i], D, Hx, N, Bx, row_el, batch_el)))
+    if (!(rank_major ? make_map5(&m.tile[i], src[i], D, H, Nl, B, P) &&
+                           make_map5(&m.quad[i], src[i], D, H, Nl, B, P, 2, 32) &&
+                           make_map5(&m.group[i], src[i], D, H, Nl, B, P, 2, 8)
+                     : make_map(&m.tile[i], src[i], D, Hx, N, Bx, row_el, batch_el)))
       return SP_ERR_CUDA;
   sp::AttnBwdParams p;
   std::memset(&p, 0, sizeof(p));
