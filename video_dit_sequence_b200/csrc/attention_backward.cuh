@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 
 #include "attention.cuh"
+#include "permute.cuh"
 #include "sm100.cuh"
 
 namespace sp {
@@ -59,6 +60,7 @@ struct AttnBwdParams {
   int32_t BH;            // B * H
   int32_t dq_tiles;      // query tiles of a dQ CTA: 1 or 2
   int32_t nl_split;      // as in AttnParams
+  FastDiv div_nl;
   float scale, scale_log2e;
   const uint8_t *q, *k, *v, *o, *dout;
   const float *lse;      // [B][H][Np]
@@ -80,7 +82,7 @@ __device__ __forceinline__ int64_t bwd_row(const AttnBwdParams &p, int bh, int t
   const int hs = hg / p.hsplit, head = hg - hs * p.hsplit;
   int64_t off;
   if (p.nl_split) {
-    const int rk = t / p.nl_split;
+    const int rk = fdiv(t, p.div_nl);
     off = rk * p.rank_el + b * p.batch_el + (t - rk * p.nl_split) * p.row_el;
   } else {
     off = (static_cast<int64_t>(hs) * p.B + b) * p.batch_el + t * p.row_el;
@@ -280,22 +282,24 @@ attention_backward_kernel(const __grid_constant__ AttnBwdMaps maps,
       if (lane < 4) prefetch_tmap(&maps.tile[lane]);
       // Rank-major layout: a tile that crosses a shard boundary, or holds
       // padding slots of the last shard, is loaded in pieces.
+      auto rank_of = [&](int n) { return static_cast<int>(fdiv(n, p.div_nl)); };
       auto tma_ok = [&](int tok) {
         if (nl == 0) return true;
-        const int r0 = tok / nl;
+        const int r0 = rank_of(tok);
         return tok - r0 * nl + 128 <= nl && tok + 128 <= p.N;
       };
       // Lane g has group g, eight rows, 1,024 bytes of each column block as the
       // TMA swizzles it.  Four groups, or one, that lie within a shard or past N
       // (zeros, from a box past the shard) are one more TMA load a column block;
       // the few others are copied row by row, 16-byte chunk cc of row r to chunk
-      // cc ^ (r mod 8).  With all rows copied so a tile took 3 us (2,050 tokens in
-      // 8 shards, 2 x 8 heads: 160 us), and through registers, four loads in
-      // flight, 6; single rows by TMA were slower than copies (150 us).
+      // cc ^ (r mod 8).  2,050 tokens in 8 shards, 2 x 8 heads: 123 us (in one
+      // shard 112); all rows copied 160; groups by TMA but not fours 140; single
+      // rows by TMA too 150.  Shards of 6 tokens (all rows copied): 58 us where a
+      // copy that steps through the rows took 49.
       auto load_pieces = [&](int which, const uint8_t *base, uint32_t dst, uint32_t bar, int tok,
                              uint64_t pol) {
         auto whole = [&](int n, int rows) {
-          return nl >= rows && (n >= p.N || (n % nl + rows <= nl && n + rows <= p.N));
+          return nl >= rows && (n >= p.N || (n - rank_of(n) * nl + rows <= nl && n + rows <= p.N));
         };
         const int n0 = tok + 8 * lane;
         const bool quad = lane < 16 && whole(tok + 32 * (lane >> 2), 32);
@@ -305,7 +309,7 @@ attention_backward_kernel(const __grid_constant__ AttnBwdMaps maps,
         __syncwarp();
         if (quad ? (lane & 3) == 0 : tma) {
           const CUtensorMap *m = quad ? &maps.quad[which] : &maps.group[which];
-          const int rk = n0 >= p.N ? 0 : n0 / nl, loc = n0 >= p.N ? nl : n0 - rk * nl;
+          const int rk = n0 >= p.N ? 0 : rank_of(n0), loc = n0 >= p.N ? nl : n0 - rk * nl;
           for (int h = 0; h < C::kHalves; ++h)
             tma_load_5d(dst + h * C::kBlockBytes + lane * 1024, m, bar, h * 64, map_head, loc, b, rk,
                         pol);
@@ -318,7 +322,7 @@ attention_backward_kernel(const __grid_constant__ AttnBwdMaps maps,
           const int g8 = 8 * (__ffs(rest) - 1);
 #pragma unroll
           for (int i = lane / kChunks; i < 8; i += 32 / kChunks) {
-            const int n = tok + g8 + i, rk = n / nl;
+            const int n = tok + g8 + i, rk = rank_of(n);
             const bool in = n < p.N;
             const uint8_t *src = base + cc * 16 +
                                  2 * (rk * p.rank_el + b * p.batch_el + (n - rk * nl) * p.row_el +
@@ -342,7 +346,7 @@ attention_backward_kernel(const __grid_constant__ AttnBwdMaps maps,
             if (nl == 0) {
               tma_load_4d(dst + h * C::kBlockBytes, m, bar, h * 64, map_head, tok, map_batch, pol);
             } else {
-              const int r0 = tok / nl;
+              const int r0 = rank_of(tok);
               tma_load_5d(dst + h * C::kBlockBytes, m, bar, h * 64, map_head, tok - r0 * nl, b, r0,
                           pol);
             }

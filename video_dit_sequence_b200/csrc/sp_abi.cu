@@ -1000,6 +1000,7 @@ sp_status attention_backward(const void *q, const void *k, const void *v, const 
   };
   p.dq_tiles = rounds(1) <= rounds(2) ? 1 : 2;
   p.nl_split = rank_major ? Nl : 0;
+  p.div_nl = sp::make_fastdiv(static_cast<uint32_t>(Nl));
   p.scale = s->scale > 0.f ? s->scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.scale_log2e = p.scale * 1.4426950408889634f;
   p.q = static_cast<const uint8_t *>(q);
