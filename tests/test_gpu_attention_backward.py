@@ -118,6 +118,10 @@ CASES = [
     ("seq", 2, 200, 3, 128, 3), ("seq", 2, 255, 2, 64, 2), ("head", 2, 257, 4, 128, 4),
     ("seq", 3, 640, 2, 128, 2), ("seq", 2, 777, 6, 128, 3), ("seq", 2, 1000, 1, 64, 4),
     ("head", 3, 511, 6, 64, 3), ("seq", 2, 1537, 4, 64, 3),
+    # shards of 5, 8, 13, 29, 32, 37 and 98 tokens, some of them empty
+    ("seq", 2, 33, 2, 128, 8), ("seq", 2, 300, 2, 64, 60), ("seq", 3, 200, 1, 128, 25),
+    ("seq", 2, 300, 2, 128, 24), ("seq", 2, 260, 2, 64, 9), ("seq", 2, 500, 2, 128, 16),
+    ("seq", 2, 361, 1, 128, 10), ("seq", 2, 777, 3, 64, 8),
     # more than 16 key tiles, and more tiles than the GPU runs at once
     ("seq", 1, 2177, 1, 128, 2), ("head", 1, 2100, 8, 128, 8), ("seq", 3, 1300, 5, 128, 4),
     ("seq", 2, 2500, 3, 64, 3), ("seq", 70, 150, 3, 128, 1), ("seq", 1, 4099, 3, 128, 1),

@@ -179,8 +179,8 @@ bool make_map(CUtensorMap *m, const void *base, int D, int Hx, int N, int Bx, in
 
 // Tensor map over rank-major sequence shards [P][B][Nl][H][D] (B > 1 and
 // P > 1), dims inner to outer (D, H, Nl, B, P).  Used only for token tiles
-// that lie inside one shard; the box is box_rows rows (or Nl when smaller,
-// in which case no tile uses the map).
+// that lie inside one shard, or past one (zeros); the box is box_rows rows (or
+// Nl when smaller, in which case no tile uses the map).
 bool make_map5(CUtensorMap *m, const void *base, int D, int H, int Nl, int B, int P,
                int es = 2, int box_rows = 128) {
   EncodeTiledFn enc = encode_fn();
