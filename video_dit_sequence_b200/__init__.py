@@ -269,6 +269,16 @@ def _stream(stream, device):
     return stream.cuda_stream
 
 
+def _empty_on(stream, shape, dtype, device):
+    """A new tensor whose memory belongs to `stream` (None: the current one):
+    it is reused in that stream's order."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _resolve_device(stream, device):
     torch = _torch()
     if stream is not None:
@@ -502,48 +512,55 @@ class UlyssesRank:
         self.shape = shape
         self._bufs = {}
 
-    def _buf(self, name, shape, like):
-        torch = _torch()
-        b = self._bufs.get(name)
-        if b is None or b.device != like.device or b.dtype != like.dtype:
-            b = self._bufs[name] = torch.empty(shape, dtype=like.dtype, device=like.device)
+    def _buf(self, name, shape, like, stream=None, dtype=None):
+        """This object's buffer of that name for a phase on `stream` (None: the
+        current one).  It is allocated on the stream of the phase that first
+        asks for it, since memory that the allocator hands out may still be in
+        use by earlier work of another stream; a phase on another stream is
+        recorded, so that the memory is not reused before that phase's end."""
+        dtype = dtype or like.dtype
+        on = _stream(stream, like.device)
+        b, own = self._bufs.get(name, (None, None))
+        if b is None or b.device != like.device or b.dtype != dtype:
+            b = _empty_on(stream, shape, dtype, like.device)
+            self._bufs[name] = b, on
+        elif on != own:
+            b.record_stream(_torch().cuda.current_stream(like.device) if stream is None else stream)
         return b
 
     def send_qkv(self, q, k, v, stream=None):
         out = []
         for name, x in (("send_q", q), ("send_k", k), ("send_v", v)):
-            send = self._buf(name, self.shape.send_chunks, x)
+            send = self._buf(name, self.shape.send_chunks, x, stream)
             exchange_pack(x, send, self.shape, stream)
             out.append(send)
         return out
 
-    def recv_buffers(self, like):
-        """Three [P][B][Nl][Hl][D] buffers for the received Q, K, V chunks."""
-        return [self._buf(n, self.shape.send_chunks, like) for n in ("recv_q", "recv_k", "recv_v")]
+    def recv_buffers(self, like, stream=None):
+        """Three [P][B][Nl][Hl][D] buffers for the received Q, K, V chunks,
+        which the exchange fills on `stream`."""
+        return [self._buf(n, self.shape.send_chunks, like, stream)
+                for n in ("recv_q", "recv_k", "recv_v")]
 
     def attend(self, q, k, v, lse=None, stream=None):
-        o = self._buf("o", self.shape.send_chunks, q)
+        o = self._buf("o", self.shape.send_chunks, q, stream)
         attention_seqsharded(q, k, v, o, self.shape.head_group(), lse=lse, stream=stream)
         return o
 
     def finish(self, back, stream=None):
-        out = self._buf("out", self.shape.rank_shard, back)
+        out = self._buf("out", self.shape.rank_shard, back, stream)
         exchange_unpack(back, out, self.shape, stream)
         return out
 
     def send_grad(self, do, stream=None):
-        send = self._buf("send_do", self.shape.send_chunks, do)
+        send = self._buf("send_do", self.shape.send_chunks, do, stream)
         exchange_pack(do, send, self.shape, stream)
         return send
 
     def attend_backward(self, q, k, v, o, lse, do, stream=None):
         group = self.shape.head_group()
-        grads = [self._buf(n, self.shape.send_chunks, q) for n in ("dq", "dk", "dv")]
-        torch = _torch()
-        ws = self._bufs.get("workspace")
-        if ws is None or ws.device != q.device:
-            ws = self._bufs["workspace"] = torch.empty(attention_backward_workspace(group),
-                                                       dtype=torch.uint8, device=q.device)
+        grads = [self._buf(n, self.shape.send_chunks, q, stream) for n in ("dq", "dk", "dv")]
+        ws = self._buf("workspace", attention_backward_workspace(group), q, stream, _torch().uint8)
         attention_backward_seqsharded(q, k, v, o, lse, do, *grads, group, workspace=ws,
                                       stream=stream)
         return grads
@@ -551,7 +568,7 @@ class UlyssesRank:
     def finish_grads(self, back, stream=None):
         out = []
         for name, b in zip(("grad_q", "grad_k", "grad_v"), back):
-            out.append(self._buf(name, self.shape.rank_shard, b))
+            out.append(self._buf(name, self.shape.rank_shard, b, stream))
             exchange_unpack(b, out[-1], self.shape, stream)
         return out
 
@@ -565,7 +582,7 @@ class UlyssesRank:
         all_to_all(self.send_grad(do), recv)
         back = []
         for name, g in zip(("back_dq", "back_dk", "back_dv"),
-                           self.attend_backward(q, k, v, self._bufs["o"], lse, recv)):
+                           self.attend_backward(q, k, v, self._bufs["o"][0], lse, recv)):
             back.append(self._buf(name, self.shape.send_chunks, g))
             all_to_all(g, back[-1])
         return self.finish_grads(back)
@@ -687,8 +704,7 @@ def _workspace(workspace, nbytes, device, stream):
     memory is reused in that stream's order."""
     torch = _torch()
     if workspace is None:
-        with torch.cuda.stream(stream):   # None: the current stream stays
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return _empty_on(stream, nbytes, torch.uint8, device)
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace must be a CUDA tensor")
     if workspace.device != device:
