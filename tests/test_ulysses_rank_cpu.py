@@ -80,3 +80,126 @@ def test_buffers_belong_to_the_stream_of_their_phase(monkeypatch):
     fake.recorded.clear()
     rank.send_grad(x)                       # (the current stream)
     assert fake.recorded == [(bufs[5].data_ptr(), 0)]
+
+
+def _plain_ptr(t, shape, name, dtype=None):
+    """The binding's checks of an operand, without a device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != (dtype or torch.bfloat16):
+        raise TypeError(f"{name} must be {dtype or torch.bfloat16}, got {t.dtype}")
+    if not t.is_contiguous() or t.numel() != torch.Size(shape).numel():
+        raise ValueError(f"{name} has shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _pack(x, send, shape, stream=None):
+    """[B][Nl][H][D] -> [P][B][Nl][Hl][D]"""
+    B, Nl, H, D = shape.rank_shard
+    send.copy_(x.reshape(B, Nl, shape.P, H // shape.P, D).permute(2, 0, 1, 3, 4))
+
+
+def _unpack(recv, out, shape, stream=None):
+    out.copy_(recv.permute(1, 2, 0, 3, 4).reshape(out.shape))
+
+
+def _heads(x, shape):
+    """[P][B][Nl][H][D] -> [B][H][N][D] in 64 bits."""
+    full = x.double().transpose(0, 1).reshape(shape.B, shape.Np, shape.H, shape.D)
+    return full[:, :shape.N].transpose(1, 2)
+
+
+def _back(x, shape):
+    full = x.new_zeros(shape.B, shape.Np, shape.H, shape.D)
+    full[:, :shape.N] = x.transpose(1, 2)
+    return full.view(shape.B, shape.P, shape.Nl, shape.H, shape.D).transpose(0, 1)
+
+
+def _attend(q, k, v, o, shape, lse=None, stream=None):
+    qd, kd, vd = (_heads(t, shape) for t in (q, k, v))
+    s = qd @ kd.transpose(2, 3) / shape.D ** 0.5
+    o.copy_(_back(torch.softmax(s, -1) @ vd, shape))
+    if lse is not None:
+        lse.fill_(float("-inf"))
+        lse[..., :shape.N] = torch.logsumexp(s, -1)
+
+
+def _attend_backward(q, k, v, o, lse, do, dq, dk, dv, shape, workspace=None, stream=None):
+    qd, kd, vd, od, dod = (_heads(t, shape) for t in (q, k, v, o, do))
+    f = shape.D ** -0.5
+    p = torch.exp(f * qd @ kd.transpose(2, 3) - lse[..., :shape.N, None].double())
+    ds = p * (dod @ vd.transpose(2, 3) - (dod * od).sum(-1, keepdim=True))
+    for out, g in ((dq, f * ds @ kd), (dk, f * ds.transpose(2, 3) @ qd), (dv, p.transpose(2, 3) @ dod)):
+        out.copy_(_back(g, shape))
+
+
+def _play(patch):
+    """The local phases in plain torch, on the current (only) stream."""
+    for name, f in (("exchange_pack", _pack), ("exchange_unpack", _unpack),
+                    ("attention_seqsharded", _attend), ("_stream", lambda s, device: 0),
+                    ("attention_backward_seqsharded", _attend_backward), ("_ptr", _plain_ptr),
+                    ("attention_backward_workspace", lambda shape: 64)):
+        patch(sp, name, f)
+
+
+def _inputs(shape, seed, n=4):
+    """n tensors [P][B][Nl][H][D] with zero padding."""
+    g = torch.Generator().manual_seed(seed)
+    return [_back(torch.randn(shape.B, shape.H, shape.N, shape.D, generator=g), shape).to(torch.bfloat16)
+            for _ in range(n)]
+
+
+def _copy(send, recv):
+    recv.copy_(send)
+
+
+def test_backward_step_goes_back_over_what_attend_took(monkeypatch):
+    """attend as a phase, on the caller's own tensors: backward_step uses
+    those, and no buffer that nothing was written to."""
+    _play(monkeypatch.setattr)
+    shape = sp.Shape(2, 9, 2, 64, 1)
+    q, k, v, do = _inputs(shape, 1)
+    rank, lse = sp.UlyssesRank(shape), torch.empty(shape.lse_shape)
+    o = rank.attend(q, k, v, lse=lse)
+    got = rank.backward_step(do[0], lse, _copy)
+    want = [torch.empty_like(q) for _ in range(3)]
+    _attend_backward(q, k, v, o, lse, do, *want, shape)
+    assert all(torch.equal(g, w[0]) for g, w in zip(got, want))
+
+
+def test_backward_step_refuses_and_keeps_the_step(monkeypatch):
+    _play(monkeypatch.setattr)
+    shape = sp.Shape(2, 9, 2, 64, 1)
+    q, k, v, do = (t[0] for t in _inputs(shape, 2))
+    lse, other = torch.empty(shape.lse_shape), torch.empty(shape.lse_shape)
+    rank = sp.UlyssesRank(shape)
+    rank.step(q, k, v, _copy, lse=lse)
+    want = [g.clone() for g in rank.backward_step(do, lse, _copy)]
+    exchanges = []
+    for bad in (do.float(), do[:1], do.transpose(0, 1), None):
+        with pytest.raises((TypeError, ValueError)):
+            rank.backward_step(bad, lse, lambda *a: exchanges.append(a))
+    for bad in (None, other):
+        with pytest.raises(ValueError, match="lse"):
+            rank.backward_step(do, bad, lambda *a: exchanges.append(a))
+    assert not exchanges
+    # a correct call after a refused one
+    assert all(torch.equal(g, w) for g, w in zip(rank.backward_step(do, lse, _copy), want))
+    # a later step that kept no lse, or another one
+    rank.step(k, q, v, _copy)
+    with pytest.raises(RuntimeError, match="kept none"):
+        rank.backward_step(do, lse, _copy)
+    rank.step(k, q, v, _copy, lse=other)
+    with pytest.raises(ValueError, match="lse"):
+        rank.backward_step(do, lse, _copy)
+    # a step that broke off, one that has only begun
+    def broken(send, recv):
+        raise OSError("peer left")
+    with pytest.raises(OSError):
+        rank.step(q, k, v, broken, lse=lse)
+    with pytest.raises(RuntimeError, match="there was none"):
+        rank.backward_step(do, other, _copy)
+    rank.step(q, k, v, _copy, lse=lse)
+    rank.recv_buffers(q)
+    with pytest.raises(RuntimeError, match="there was none"):
+        rank.backward_step(do, lse, _copy)

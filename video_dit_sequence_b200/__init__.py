@@ -511,6 +511,7 @@ class UlyssesRank:
     def __init__(self, shape: Shape):
         self.shape = shape
         self._bufs = {}
+        self._last = None   # (q, k, v, o, lse) of the last attend
 
     def _buf(self, name, shape, like, stream=None, dtype=None):
         """This object's buffer of that name for a phase on `stream` (None: the
@@ -538,13 +539,16 @@ class UlyssesRank:
 
     def recv_buffers(self, like, stream=None):
         """Three [P][B][Nl][Hl][D] buffers for the received Q, K, V chunks,
-        which the exchange fills on `stream`."""
+        which the exchange fills on `stream`: a new step begins."""
+        self._last = None
         return [self._buf(n, self.shape.send_chunks, like, stream)
                 for n in ("recv_q", "recv_k", "recv_v")]
 
     def attend(self, q, k, v, lse=None, stream=None):
+        self._last = None
         o = self._buf("o", self.shape.send_chunks, q, stream)
         attention_seqsharded(q, k, v, o, self.shape.head_group(), lse=lse, stream=stream)
+        self._last = q, k, v, o, lse
         return o
 
     def finish(self, back, stream=None):
@@ -573,16 +577,26 @@ class UlyssesRank:
         return out
 
     def backward_step(self, do, lse, all_to_all):
-        """The way back of the last step, which was given this lse: returns the
-        gradients of its q, k and v shards (this object's buffers)."""
-        if "o" not in self._bufs:
+        """The way back of the last step (or attend), which was given this lse
+        tensor, through the very tensors that it attended with: returns the
+        gradients of its q, k and v shards (this object's buffers).  Refuses,
+        before any exchange, a step that kept no lse or another one, and a do
+        that is not a shard like the step's output."""
+        if self._last is None:
             raise RuntimeError("backward_step goes back over a step: there was none")
-        q, k, v = self.recv_buffers(do)
+        q, k, v, o, kept = self._last
+        if kept is None:
+            raise RuntimeError("backward_step needs the lse of the last step, which kept none")
+        if not isinstance(lse, _torch().Tensor) or lse.data_ptr() != kept.data_ptr():
+            raise ValueError("lse is not the tensor that the last step was given")
+        _ptr(do, self.shape.rank_shard, "do")
+        if do.device != q.device:
+            raise ValueError(f"operands on several devices: {do.device}, {q.device}")
         recv = self._buf("recv_do", self.shape.send_chunks, do)
         all_to_all(self.send_grad(do), recv)
         back = []
         for name, g in zip(("back_dq", "back_dk", "back_dv"),
-                           self.attend_backward(q, k, v, self._bufs["o"][0], lse, recv)):
+                           self.attend_backward(q, k, v, o, kept, recv)):
             back.append(self._buf(name, self.shape.send_chunks, g))
             all_to_all(g, back[-1])
         return self.finish_grads(back)
