@@ -51,3 +51,70 @@ def test_phases_on_a_stream_of_their_own():
     assert side.cuda_stream != torch.cuda.current_stream().cuda_stream
     assert all(_stream_of(t) == side.cuda_stream for t in got)
     assert sp.device_status() == sp.SP_OK
+
+
+@pytest.mark.parametrize("B,N,H,D,P", [(1, 700, 4, 128, 4), (2, 333, 6, 64, 3), (2, 9, 8, 64, 8)])
+def test_there_and_back_on_virtual_ranks(B, N, H, D, P):
+    """step and backward_step of P ranks, a thread each, whose exchanges meet
+    at a host barrier and copy chunks on the one stream they share (no kernel
+    waits for another): bit-equal to the calls on all shards, twice in a row
+    with the same objects."""
+    import threading
+    shape = sp.Shape(B, N, H, D, P)
+    ranks = [sp.UlyssesRank(shape) for _ in range(P)]
+    lses = [torch.empty(shape.head_group().lse_shape, device="cuda") for _ in ranks]
+    for seed in (5, 6):
+        q, k, v, do = _shards(shape, 4, seed)
+        o, lse = torch.empty_like(q), torch.empty(shape.lse_shape, device="cuda")
+        sp.attention_seqsharded(q, k, v, o, shape, lse=lse)
+        want = [torch.empty_like(q) for _ in range(3)]
+        sp.attention_backward_seqsharded(q, k, v, o, lse, do, *want, shape)
+        barrier, sent, got, errors = threading.Barrier(P), [None] * P, [None] * P, []
+
+        def main(r):
+            def exchange(send, recv):
+                sent[r] = send
+                barrier.wait(60)           # every rank's pack is enqueued
+                for i in range(P):
+                    recv[i].copy_(sent[i][r])
+                barrier.wait(60)           # every copy is, before a buffer is packed again
+            try:
+                out = ranks[r].step(q[r], k[r], v[r], exchange, lse=lses[r])
+                got[r] = [out] + ranks[r].backward_step(do[r], lses[r], exchange)
+            except BaseException as e:
+                errors.append(e)
+                barrier.abort()
+
+        threads = [threading.Thread(target=main, args=(r,)) for r in range(P)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join(120)
+        assert not errors, errors
+        torch.cuda.synchronize()
+        for r in range(P):
+            assert all(torch.equal(g, w[r]) for g, w in zip(got[r], [o] + want)), (seed, r)
+        assert torch.equal(torch.cat(lses, 1)[..., :N], lse[..., :N])
+    assert sp.device_status() == sp.SP_OK
+
+
+def test_refused_way_back():
+    """A dO or lse that does not fit is refused before any exchange, and the
+    call with the right ones gives the step's gradients all the same."""
+    shape = sp.Shape(1, 200, 2, 64, 1)
+    q, k, v, do = (t[0] for t in _shards(shape, 4, seed=8))
+    rank, lse = sp.UlyssesRank(shape), torch.empty(shape.lse_shape, device="cuda")
+    copy = lambda send, recv: recv.copy_(send)
+    rank.step(q, k, v, copy, lse=lse)
+    want = [g.clone() for g in rank.backward_step(do, lse, copy)]
+    calls = []
+    refuse = lambda send, recv: calls.append(send)
+    for bad in (do.float(), do.cpu(), do[:, :-1], do.transpose(1, 2)):
+        with pytest.raises((TypeError, ValueError)):
+            rank.backward_step(bad, lse, refuse)
+    for bad in (None, lse.clone()):
+        with pytest.raises(ValueError):
+            rank.backward_step(do, bad, refuse)
+    assert not calls
+    assert all(torch.equal(g, w) for g, w in zip(rank.backward_step(do, lse, copy), want))
+    assert sp.device_status() == sp.SP_OK

@@ -145,8 +145,8 @@ def _play(patch):
 def _inputs(shape, seed, n=4):
     """n tensors [P][B][Nl][H][D] with zero padding."""
     g = torch.Generator().manual_seed(seed)
-    return [_back(torch.randn(shape.B, shape.H, shape.N, shape.D, generator=g), shape).to(torch.bfloat16)
-            for _ in range(n)]
+    rows = (torch.randn(shape.B, shape.H, shape.N, shape.D, generator=g) for _ in range(n))
+    return [_back(x, shape).to(torch.bfloat16).contiguous() for x in rows]
 
 
 def _copy(send, recv):
