@@ -84,6 +84,8 @@ def test_buffers_belong_to_the_stream_of_their_phase(monkeypatch):
 
 def _plain_ptr(t, shape, name, dtype=None):
     """The binding's checks of an operand, without a device."""
+    if t is None:
+        return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != (dtype or torch.bfloat16):

@@ -589,7 +589,8 @@ class UlyssesRank:
             raise RuntimeError("backward_step needs the lse of the last step, which kept none")
         if not isinstance(lse, _torch().Tensor) or lse.data_ptr() != kept.data_ptr():
             raise ValueError("lse is not the tensor that the last step was given")
-        _ptr(do, self.shape.rank_shard, "do")
+        if _ptr(do, self.shape.rank_shard, "do") is None:
+            raise TypeError("do must be a CUDA tensor")
         if do.device != q.device:
             raise ValueError(f"operands on several devices: {do.device}, {q.device}")
         recv = self._buf("recv_do", self.shape.send_chunks, do)
