@@ -205,3 +205,16 @@ def test_backward_step_refuses_and_keeps_the_step(monkeypatch):
     rank.recv_buffers(q)
     with pytest.raises(RuntimeError, match="there was none"):
         rank.backward_step(do, lse, _copy)
+
+
+def test_step_refuses_an_lse_before_any_exchange(monkeypatch):
+    """(The other ranks would wait in an exchange that this one never joins.)"""
+    _play(monkeypatch.setattr)
+    shape = sp.Shape(2, 9, 2, 64, 1)
+    q, k, v, _ = (t[0] for t in _inputs(shape, 2))
+    exchanges = []
+    for bad in (torch.empty(shape.lse_shape).double(), torch.empty(shape.lse_shape)[..., 1:],
+                torch.empty(2, 2, 10)[..., :9], torch.empty(shape.lse_shape, device="meta")):
+        with pytest.raises((TypeError, ValueError)):
+            sp.UlyssesRank(shape).step(q, k, v, lambda *a: exchanges.append(a), lse=bad)
+    assert not exchanges

@@ -605,7 +605,11 @@ class UlyssesRank:
     def step(self, q, k, v, all_to_all, lse=None):
         """The whole step with all_to_all(send, recv) filling recv: returns
         this rank's output shard (this object's buffer).  lse ([B][Hl][Np]
-        float32), if given, is filled for backward_step."""
+        float32), if given, is filled for backward_step; one that does not fit
+        is refused before any exchange."""
+        _ptr(lse, self.shape.head_group().lse_shape, "lse", _torch().float32)
+        if lse is not None and lse.device != q.device:
+            raise ValueError(f"operands on several devices: {lse.device}, {q.device}")
         recv = self.recv_buffers(q)
         for send, r in zip(self.send_qkv(q, k, v), recv):
             all_to_all(send, r)
