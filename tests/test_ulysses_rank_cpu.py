@@ -218,3 +218,14 @@ def test_step_refuses_an_lse_before_any_exchange(monkeypatch):
         with pytest.raises((TypeError, ValueError)):
             sp.UlyssesRank(shape).step(q, k, v, lambda *a: exchanges.append(a), lse=bad)
     assert not exchanges
+
+
+def test_distributed_call_keeps_an_lse(monkeypatch):
+    _play(monkeypatch.setattr)
+    shape = sp.Shape(1, 9, 2, 64, 1)
+    q, k, v, do = (t[0] for t in _inputs(shape, 3))
+    rank, lse = sp.UlyssesRank(shape), torch.empty(shape.lse_shape)
+    out = sp.ulysses_attention_distributed(q, k, v, shape, all_to_all=_copy, rank=rank, lse=lse)
+    got = [out.clone()] + [g.clone() for g in rank.backward_step(do, lse, _copy)]
+    want = [rank.step(q, k, v, _copy, lse=lse)] + rank.backward_step(do, lse, _copy)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

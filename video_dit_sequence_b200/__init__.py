@@ -1170,15 +1170,17 @@ def nccl_all_to_all(group=None):
     return exchange
 
 
-def ulysses_attention_distributed(q, k, v, shape: Shape, all_to_all=None, rank=None):
+def ulysses_attention_distributed(q, k, v, shape: Shape, all_to_all=None, rank=None, lse=None):
     """One rank's Ulysses attention step: q, k, v are this rank's shards
     [B][Nl][H][D] (rank = position in the group of shape.P ranks); returns
     the output shard.  all_to_all defaults to NCCL over the default group.
     Pass the same UlyssesRank as `rank` on every step to reuse its buffers
-    (the returned shard is then overwritten by the next step)."""
+    (the returned shard is then overwritten by the next step); given an
+    lse ([B][Hl][Np] float32) to fill, its backward_step goes back over this
+    step."""
     all_to_all = all_to_all or nccl_all_to_all()
     rank = rank or UlyssesRank(shape)
-    return rank.step(q, k, v, all_to_all)
+    return rank.step(q, k, v, all_to_all, lse=lse)
 
 
 class StepPipeline:
