@@ -758,7 +758,8 @@ sp::LnParams norm_params(const sp_shape *s, int32_t hidden, int32_t param_layout
   p.per_sample = param_layout == SP_PARAM_PER_SAMPLE;
   p.linear = p.B == 1 || p.P == 1;
   p.param_f32 = param_type == SP_PARAM_FP32;
-  p.inv_c = 1.0f / static_cast<float>(hidden);
+  p.c = static_cast<float>(hidden);
+  p.inv_c = 1.0f / p.c;
   return p;
 }
 
