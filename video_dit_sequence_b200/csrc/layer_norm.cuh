@@ -342,10 +342,11 @@ layer_norm_backward_kernel(const LnParams p, int tn) {
   for (; i - sub < nrows; i += teams, ph ^= 2) {  // (the same steps in all lanes)
     cp_async_wait_group<K - 2>();
     const bool row_in = !kSub || i < nrows;
-    // xh = x rstd + shift: one rounding more on the mean's share, like the
-    // mean's own
-    const float rs = rstd, shift = -mean * rstd;
-    const uint64_t rstd2 = f2_pack(rs, rs), shift2 = f2_pack(shift, shift);
+    // xh = (x - mean) rstd, in this order in both sweeps: x rstd - mean rstd
+    // would be off by the product's rounding, |mean| rstd 2^-24 (0.4 in a constant
+    // row of 9,984), where x - mean is exact
+    const float rs = rstd;
+    const uint64_t rstd2 = f2_pack(rs, rs), nmean2 = f2_pack(-mean, -mean);
     uint4 *dx = p.y + row * p.C8;
     // g stays in registers for the second sweep, or dy packed when V = 4
     // (kept, its 16 registers spilled)
@@ -370,7 +371,7 @@ layer_norm_backward_kernel(const LnParams p, int tn) {
       ln_load_params(sw, p.C8, in ? c : 0, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t xh = f2_fma(x[e], rstd2, shift2);
+        const uint64_t xc = f2_add(x[e], nmean2), xh = f2_mul(xc, rstd2);
         const uint64_t gv = f2_mul(d[e], w[e]);   // (0 past the row)
         if (kKeep) gk[kKeep ? v : 0][e] = gv;
         a1 = f2_add(a1, gv);
@@ -387,9 +388,9 @@ layer_norm_backward_kernel(const LnParams p, int tn) {
     float sums[2] = {f2_sum(a1), f2_sum(a2)};
     team_sums<2, kSub>(sums, red + ph, team, tn);
     if (!row_in) continue;
-    // dx = rstd (g - s1 - xh s2) = g rstd + (x a + b)
+    // dx = rstd (g - s1 - xh s2) = g rstd + ((x - mean) a + b)
     const float s1 = sums[0] * p.inv_c, s2 = sums[1] * p.inv_c;
-    const float a = -rs * rs * s2, bb = -rs * fmaf(s2, shift, s1);
+    const float a = -rs * rs * s2, bb = -rs * s1;
     const uint64_t aa2 = f2_pack(a, a), bb2 = f2_pack(bb, bb);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -406,7 +407,8 @@ layer_norm_backward_kernel(const LnParams p, int tn) {
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          x[e] = f2_fma(kKeep ? gk[kKeep ? v : 0][e] : gv[e], rstd2, f2_fma(x[e], aa2, bb2));
+          x[e] = f2_fma(kKeep ? gk[kKeep ? v : 0][e] : gv[e], rstd2,
+                        f2_fma(f2_add(x[e], nmean2), aa2, bb2));
         dx[c] = ln_pack2(x);
       }
     }
