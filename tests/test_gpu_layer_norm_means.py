@@ -114,3 +114,21 @@ def test_one_value_stands_out(C):
     err = 100 * U * r * (gd.abs() + gd.abs().mean(1, keepdim=True)
                         + xh.abs() * (gd * xh).abs().mean(1, keepdim=True))
     assert ((dx.double() - ref).abs() <= 2.0 ** -8 * (ref.abs() + err) + err).all()
+
+
+@pytest.mark.parametrize("C", [24, 40, 104, 200, 264, 328])
+def test_rows_whose_mean_over_their_deviation_is_past_fp32(C):
+    """Constant rows of 1e36: mean * rstd is infinite, and lanes of a team that
+    have no columns must not bring that into the row's sums."""
+    x = torch.full((70, C), 1e36, device="cuda").to(torch.bfloat16)
+    w, b = _params(C, 5)
+    dy = torch.randn(x.shape, generator=torch.Generator(device="cuda").manual_seed(6),
+                     device="cuda").to(torch.bfloat16)
+    shape, y, mean, rstd = _forward(x, w, b)
+    assert torch.equal(mean, x[:, 0].float()) and torch.equal(y, b.to(torch.bfloat16).expand_as(y))
+    dx, dw, db = _backward(x, dy, w, shape, mean, rstd)
+    assert (dw == 0).all()
+    gd = dy.double() * w.double()
+    ref = 1e3 * (gd - gd.mean(1, keepdim=True))
+    err = 1e3 * 48 * U * (gd.abs() + gd.abs().mean(1, keepdim=True))   # (as above)
+    assert ((dx.double() - ref).abs() <= 2.0 ** -8 * (ref.abs() + err) + err).all()

@@ -358,6 +358,9 @@ layer_norm_backward_kernel(const LnParams p, int tn) {
     for (int v = 0; v < V; ++v) {
       const int c = tt + v * tn;
       const bool in = row_in && c < p.C8;
+      // past the row, where only a last vector can be, x - mean is 0 as dy is: 0
+      // times -mean rstd is NaN where that product is past fp32 (a row of 1e36)
+      const uint64_t center2 = v < V - 1 || in ? nmean2 : zero2;
       uint4 dp = make_uint4(0u, 0u, 0u, 0u);
       xp[v] = dp;
       if (in) {
@@ -371,7 +374,7 @@ layer_norm_backward_kernel(const LnParams p, int tn) {
       ln_load_params(sw, p.C8, in ? c : 0, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t xc = f2_add(x[e], nmean2), xh = f2_mul(xc, rstd2);
+        const uint64_t xh = f2_mul(f2_add(x[e], center2), rstd2);
         const uint64_t gv = f2_mul(d[e], w[e]);   // (0 past the row)
         if (kKeep) gk[kKeep ? v : 0][e] = gv;
         a1 = f2_add(a1, gv);
