@@ -300,8 +300,7 @@ typedef enum { SP_PARAM_BF16 = 0, SP_PARAM_FP32 = 1 } sp_param_type;
  * transformer modulates each generation's norm by its own scale and shift).
  * fp32 arithmetic, one rounding to bf16.  The result does not depend on P.
  * x: device bf16 [P][B][Nl][hidden], the sequence-sharded hidden states, read
- *   only; padding slots (tokens at or past N) are not read.  One rank's shard
- *   [B][Nl][hidden] is the problem {B, Nl, ..., P = 1}.
+ *   only; padding slots (tokens at or past N) are not read.
  * weight, bias: device parameters of param_layout and param_type, or NULL
  *   (weight 1, bias 0), each on its own.
  * y: device bf16, as x, written in full (padding slots +0.0); not x.
@@ -314,6 +313,16 @@ typedef enum { SP_PARAM_BF16 = 0, SP_PARAM_FP32 = 1 } sp_param_type;
 sp_status sp_layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
                         float *rstd, int32_t hidden, float eps, int32_t param_layout,
                         int32_t param_type, const sp_shape *shape, void *stream);
+
+/* sp_layer_norm of one rank's shard, when every rank is its own GPU: x and y
+ * are [B][Nl][hidden], mean and rstd [B][Nl], tokens rank*Nl .. of the problem
+ * `shape`; slots at or past N (any number of them, in the last ranks) are
+ * padding as above.  Equal, bit for bit, to that shard of the call on all
+ * shards.  rank outside [0, P): SP_ERR_SHAPE. */
+sp_status sp_layer_norm_rank(const void *x, const void *weight, const void *bias, void *y,
+                             float *mean, float *rstd, int32_t hidden, float eps,
+                             int32_t param_layout, int32_t param_type, int32_t rank,
+                             const sp_shape *shape, void *stream);
 
 /* Bytes of the workspace of sp_layer_norm_backward, for either parameter
  * layout; -1 when the shape or hidden is out of range. */
@@ -341,6 +350,19 @@ sp_status sp_layer_norm_backward(const void *dy, const void *x, const void *weig
                                  void *dbias, void *workspace, int32_t hidden,
                                  int32_t param_layout, int32_t param_type, const sp_shape *shape,
                                  void *stream);
+
+/* sp_layer_norm_backward of one rank's shard: dy, x and dx are
+ * [B][Nl][hidden], mean and rstd [B][Nl], as for sp_layer_norm_rank.  dx is that
+ * shard of the call on all shards, bit for bit; dweight and dbias are the sums
+ * over this rank's tokens (0 when it has none), which the caller adds up over
+ * the ranks.
+ * workspace: sp_layer_norm_backward_workspace bytes of the problem
+ *   {B, Nl, H, D, 1}. */
+sp_status sp_layer_norm_backward_rank(const void *dy, const void *x, const void *weight,
+                                      const float *mean, const float *rstd, void *dx,
+                                      void *dweight, void *dbias, void *workspace, int32_t hidden,
+                                      int32_t param_layout, int32_t param_type, int32_t rank,
+                                      const sp_shape *shape, void *stream);
 
 /* Tokens per cube of the block-sparse call's mask, and the most cubes
  * (ceil(N / SP_SPARSE_CUBE)) the call takes: 524,288 tokens. */

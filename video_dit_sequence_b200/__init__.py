@@ -48,7 +48,8 @@ EXPORTED = ("sp_padded_tokens", "sp_check_shape", "sp_pack", "sp_unpack",
             "sp_attention_sparse_seqsharded", "sp_qkv_projection", "sp_out_projection",
             "sp_exchange_push", "sp_attention_ulysses_overlap", "sp_shard", "sp_unshard",
             "sp_copy_heads", "sp_layer_norm", "sp_layer_norm_backward",
-            "sp_layer_norm_backward_workspace", "sp_attention_backward",
+            "sp_layer_norm_backward_workspace", "sp_layer_norm_rank",
+            "sp_layer_norm_backward_rank", "sp_attention_backward",
             "sp_attention_backward_seqsharded", "sp_attention_backward_workspace")
 
 
@@ -99,10 +100,14 @@ def load(path: str = LIB_PATH):
     i32 = ctypes.c_int32
     lib.sp_layer_norm.argtypes = [vp] * 6 + [i32, ctypes.c_float, i32, i32, sp_p, vp]
     lib.sp_layer_norm.restype = ctypes.c_int
+    lib.sp_layer_norm_rank.argtypes = [vp] * 6 + [i32, ctypes.c_float, i32, i32, i32, sp_p, vp]
+    lib.sp_layer_norm_rank.restype = ctypes.c_int
     lib.sp_layer_norm_backward_workspace.argtypes = [sp_p, i32]
     lib.sp_layer_norm_backward_workspace.restype = ctypes.c_int64
     lib.sp_layer_norm_backward.argtypes = [vp] * 9 + [i32, i32, i32, sp_p, vp]
     lib.sp_layer_norm_backward.restype = ctypes.c_int
+    lib.sp_layer_norm_backward_rank.argtypes = [vp] * 9 + [i32, i32, i32, i32, sp_p, vp]
+    lib.sp_layer_norm_backward_rank.restype = ctypes.c_int
     for fn in (lib.sp_attention_backward, lib.sp_attention_backward_seqsharded):
         fn.argtypes = [vp] * 10 + [sp_p, vp]
         fn.restype = ctypes.c_int
@@ -760,17 +765,28 @@ def _norm_params(params, shape: Shape, hidden: int):
     return int(per_sample), int(fp32), dtype, pshape
 
 
+def _norm_call(name, rank, shape):
+    """(library call, its name, shape of the rows, further arguments) of a norm
+    on all shards, or on one rank's."""
+    if rank is None:
+        return getattr(load(), name), name, shape.seq_sharded[:3], ()
+    name += "_rank"
+    return getattr(load(), name), name, shape.rank_shard[:2], (int(rank),)
+
+
 def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: float = 1e-6,
-               stream=None):
+               stream=None, rank=None):
     """Layer norm of the hidden states (sp_layer_norm): x and y bf16
     [P][B][Nl][hidden]; weight and bias [hidden], or [B][hidden] for a
     modulation of its own per sample, bf16 or float32, or None; mean and rstd
     receive the rows' statistics (float32 [P][B][Nl]) for the backward
-    pass."""
+    pass.  With a rank, x, y, mean and rstd are that rank's shard of them,
+    [B][Nl]... (sp_layer_norm_rank), whose slots past N are padding too."""
     torch = _torch()
     dev = _device_of(x, "x")
     hidden = x.shape[-1]
-    bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
+    fn, name, rows, more = _norm_call("sp_layer_norm", rank, shape)
+    bf16, f32 = torch.bfloat16, torch.float32
     full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, bias), shape, hidden)
     n = math.prod(rows)
@@ -778,14 +794,14 @@ def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: floa
     ops = _operands(dev, ("x", "weight", "bias", "y", "mean", "rstd"),
                     (x, weight, bias, y, mean, rstd), (bf16, dtype, dtype, bf16, f32, f32),
                     (nx, nw, nw, nx, n, n), (full, pshape, pshape, full, rows, rows))
-    _call(load().sp_layer_norm, "sp_layer_norm", dev, *ops, hidden, float(eps), layout, ptype,
-          ctypes.byref(shape.c()), _stream(stream, dev))
+    _call(fn, name, dev, *ops, hidden, float(eps), layout, ptype, *more, ctypes.byref(shape.c()),
+          _stream(stream, dev))
 
 
 @functools.lru_cache(maxsize=256)
-def layer_norm_backward_workspace(shape: Shape, hidden: int) -> int:
-    """Bytes of layer_norm_backward's workspace."""
-    s = shape.c()
+def layer_norm_backward_workspace(shape: Shape, hidden: int, rank=None) -> int:
+    """Bytes of layer_norm_backward's workspace (the same for every rank)."""
+    s = (shape if rank is None else Shape(shape.B, shape.Nl, shape.H, shape.D, 1)).c()
     n = int(load().sp_layer_norm_backward_workspace(ctypes.byref(s), int(hidden)))
     if n < 0:
         raise SpError(SP_ERR_SHAPE, "sp_layer_norm_backward_workspace")
@@ -793,16 +809,19 @@ def layer_norm_backward_workspace(shape: Shape, hidden: int) -> int:
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=None, dbias=None,
-                        workspace=None, stream=None):
+                        workspace=None, stream=None, rank=None):
     """Backward pass of layer_norm (sp_layer_norm_backward): dx receives the
     gradient of x, dweight and dbias (both or neither; shape and type of the
     parameters) the sums over the tokens.  workspace: a CUDA tensor of at
     least layer_norm_backward_workspace bytes to reuse (one per call in
-    flight), else a fresh one."""
+    flight), else a fresh one.  With a rank, as for layer_norm
+    (sp_layer_norm_backward_rank): dweight and dbias are the sums over that
+    rank's tokens, for the caller to add up over the ranks."""
     torch = _torch()
     dev = _device_of(x, "x")
     hidden = x.shape[-1]
-    bf16, f32, rows = torch.bfloat16, torch.float32, shape.seq_sharded[:3]
+    fn, name, rows, more = _norm_call("sp_layer_norm_backward", rank, shape)
+    bf16, f32 = torch.bfloat16, torch.float32
     full = rows + (hidden,)
     layout, ptype, dtype, pshape = _norm_params((weight, dweight, dbias), shape, hidden)
     n = math.prod(rows)
@@ -815,9 +834,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=Non
     st = _stream(stream, dev)
     ws = None
     if dweight is not None or dbias is not None:
-        ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden), dev, stream)
-    _call(load().sp_layer_norm_backward, "sp_layer_norm_backward", dev, *ops,
-          None if ws is None else ws.data_ptr(), hidden, layout, ptype, ctypes.byref(shape.c()), st)
+        ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden, rank), dev, stream)
+    _call(fn, name, dev, *ops, None if ws is None else ws.data_ptr(), hidden, layout, ptype, *more,
+          ctypes.byref(shape.c()), st)
 
 
 SPARSE_CUBE = 64         # SP_SPARSE_CUBE

@@ -731,6 +731,8 @@ sp_status launch_projection(const CUtensorMap &ma, const void *w, int slots, sp:
 }
 
 // Layer norm (see sp_layer_norm in sp.h).  Only B, N and P of the shape count.
+constexpr int32_t kAllShards = -1;  // in the place of a rank
+
 sp_status check_norm(const sp_shape *s, int32_t hidden, int32_t param_layout, int32_t param_type) {
   if (s == nullptr) return SP_ERR_NULL;
   if (s->B < 1 || s->N < 1 || s->P < 1 || s->B > 65535 || s->P > 65535) return SP_ERR_SHAPE;
@@ -744,8 +746,10 @@ sp_status check_norm(const sp_shape *s, int32_t hidden, int32_t param_layout, in
   return SP_OK;
 }
 
+// Of a rank: its tokens as those of one shard of Nl slots (maybe none of them
+// a token).
 sp::LnParams norm_params(const sp_shape *s, int32_t hidden, int32_t param_layout,
-                         int32_t param_type) {
+                         int32_t param_type, int32_t rank) {
   sp::LnParams p;
   std::memset(&p, 0, sizeof(p));
   p.C8 = hidden / 8;
@@ -753,10 +757,16 @@ sp::LnParams norm_params(const sp_shape *s, int32_t hidden, int32_t param_layout
   p.B = s->B;
   p.N = s->N;
   p.Nl = static_cast<int32_t>((static_cast<int64_t>(s->N) + s->P - 1) / s->P);
-  p.div_n = sp::make_fastdiv(static_cast<uint32_t>(p.N));
+  p.linear = p.B == 1 || p.P == 1;
+  if (rank != kAllShards) {
+    const int64_t left = s->N - static_cast<int64_t>(rank) * p.Nl;
+    p.N = static_cast<int32_t>(std::clamp<int64_t>(left, 0, p.Nl));
+    p.P = 1;
+    p.linear = p.B == 1 || p.N == p.Nl;
+  }
+  p.div_n = sp::make_fastdiv(static_cast<uint32_t>(std::max(p.N, 1)));
   p.div_nl = sp::make_fastdiv(static_cast<uint32_t>(p.Nl));
   p.per_sample = param_layout == SP_PARAM_PER_SAMPLE;
-  p.linear = p.B == 1 || p.P == 1;
   p.param_f32 = param_type == SP_PARAM_FP32;
   p.c = static_cast<float>(hidden);
   p.inv_c = 1.0f / p.c;
@@ -775,7 +785,8 @@ struct NormPlan {
   int64_t blocks;  // of a group
 };
 
-NormPlan norm_plan(const sp::LnParams &p, bool backward) {
+// tokens: of a sample, as many as the plan goes by.
+NormPlan norm_plan(const sp::LnParams &p, int32_t tokens, bool backward) {
   NormPlan pl;
   // The smallest team; backward, where registers allow few warps, a larger one
   // that leaves the block as many teams and at most a tenth of its lanes idle
@@ -789,7 +800,7 @@ NormPlan norm_plan(const sp::LnParams &p, bool backward) {
       if (10 * p.C8 >= 9 * 32 * w * vectors(w)) pl.W = w;
   pl.V = vectors(pl.W);
   pl.groups = p.per_sample ? p.B : 1;
-  const int64_t nrows = p.per_sample ? p.N : static_cast<int64_t>(p.B) * p.N;
+  const int64_t nrows = p.per_sample ? tokens : static_cast<int64_t>(p.B) * tokens;
   const int64_t slots =
       std::max<int64_t>(1, 148 * sp::ln_blocks_per_sm(pl.V, backward) / pl.groups);
   // a row of few vectors takes a part of a warp
@@ -821,16 +832,24 @@ cudaError_t for_vectors(int V, F launch) {
   }
 }
 
+// A rank's plan goes by its slots, so that all ranks have the same.
+int32_t norm_tokens(const sp::LnParams &p, int32_t rank) { return rank == kAllShards ? p.N : p.Nl; }
+
+sp_status check_norm_rank(const sp_shape *s, int32_t rank) {
+  return rank == kAllShards || (rank >= 0 && rank < s->P) ? SP_OK : SP_ERR_SHAPE;
+}
+
 sp_status layer_norm(const void *x, const void *weight, const void *bias, void *y, float *mean,
                      float *rstd, int32_t hidden, float eps, int32_t param_layout,
-                     int32_t param_type, const sp_shape *s, void *stream) {
+                     int32_t param_type, int32_t rank, const sp_shape *s, void *stream) {
   sp_status st = check_norm(s, hidden, param_layout, param_type);
+  if (st == SP_OK) st = check_norm_rank(s, rank);
   if (st != SP_OK) return st;
   if (x == nullptr || y == nullptr) return SP_ERR_NULL;
   if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias) ||
       !aligned4(mean) || !aligned4(rstd))
     return SP_ERR_ALIGN;
-  sp::LnParams p = norm_params(s, hidden, param_layout, param_type);
+  sp::LnParams p = norm_params(s, hidden, param_layout, param_type, rank);
   p.x = static_cast<const uint4 *>(x);
   p.y = static_cast<uint4 *>(y);
   p.weight = weight;
@@ -839,7 +858,7 @@ sp_status layer_norm(const void *x, const void *weight, const void *bias, void *
   p.rstd = rstd;
   p.eps = eps > 0.f ? eps : 1e-6f;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const NormPlan pl = norm_plan(p, false);
+  const NormPlan pl = norm_plan(p, norm_tokens(p, rank), false);
   return launch_status(for_vectors<sp::kLnFwdVec>(pl.V, [&](auto v) {
     static bool set[kMaxDevices] = {};
     const auto kernel = sp::layer_norm_kernel<decltype(v)::value>;
@@ -854,7 +873,8 @@ int64_t norm_backward_workspace(const sp_shape *s, int32_t hidden) {
   if (check_norm(s, hidden, SP_PARAM_SHARED, SP_PARAM_BF16) != SP_OK) return -1;
   int64_t rows = 0;
   for (int32_t layout : {SP_PARAM_SHARED, SP_PARAM_PER_SAMPLE}) {
-    const NormPlan pl = norm_plan(norm_params(s, hidden, layout, SP_PARAM_BF16), true);
+    const NormPlan pl =
+        norm_plan(norm_params(s, hidden, layout, SP_PARAM_BF16, kAllShards), s->N, true);
     rows = std::max(rows, pl.blocks * pl.groups);
   }
   return rows * 2 * hidden * 4;
@@ -892,8 +912,9 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, i
 sp_status layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
                               const float *rstd, void *dx, void *dweight, void *dbias,
                               void *workspace, int32_t hidden, int32_t param_layout,
-                              int32_t param_type, const sp_shape *s, void *stream) {
+                              int32_t param_type, int32_t rank, const sp_shape *s, void *stream) {
   sp_status st = check_norm(s, hidden, param_layout, param_type);
+  if (st == SP_OK) st = check_norm_rank(s, rank);
   if (st != SP_OK) return st;
   if (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr)
     return SP_ERR_NULL;
@@ -903,7 +924,7 @@ sp_status layer_norm_backward(const void *dy, const void *x, const void *weight,
       !aligned16(dweight) || !aligned16(dbias) || !aligned16(workspace) || !aligned4(mean) ||
       !aligned4(rstd))
     return SP_ERR_ALIGN;
-  sp::LnParams p = norm_params(s, hidden, param_layout, param_type);
+  sp::LnParams p = norm_params(s, hidden, param_layout, param_type, rank);
   p.x = static_cast<const uint4 *>(x);
   p.dy = static_cast<const uint4 *>(dy);
   p.y = static_cast<uint4 *>(dx);
@@ -914,7 +935,7 @@ sp_status layer_norm_backward(const void *dy, const void *x, const void *weight,
   p.dbias = dbias;
   p.partial = static_cast<float *>(workspace);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const NormPlan pl = norm_plan(p, true);
+  const NormPlan pl = norm_plan(p, norm_tokens(p, rank), true);
   st = launch_status(for_vectors<sp::kLnBwdVec>(pl.V, [&](auto v) {
     return grad ? launch_norm_backward<decltype(v)::value, true>(p, pl, cs)
                 : launch_norm_backward<decltype(v)::value, false>(p, pl, cs);
@@ -1189,8 +1210,18 @@ sp_status sp_layer_norm(const void *x, const void *weight, const void *bias, voi
                         float *rstd, int32_t hidden, float eps, int32_t param_layout,
                         int32_t param_type, const sp_shape *shape, void *stream) {
   NvtxRange range("sp_layer_norm");
-  return layer_norm(x, weight, bias, y, mean, rstd, hidden, eps, param_layout, param_type, shape,
-                    stream);
+  return layer_norm(x, weight, bias, y, mean, rstd, hidden, eps, param_layout, param_type,
+                    kAllShards, shape, stream);
+}
+
+sp_status sp_layer_norm_rank(const void *x, const void *weight, const void *bias, void *y,
+                             float *mean, float *rstd, int32_t hidden, float eps,
+                             int32_t param_layout, int32_t param_type, int32_t rank,
+                             const sp_shape *shape, void *stream) {
+  NvtxRange range("sp_layer_norm_rank");
+  if (rank < 0) return SP_ERR_SHAPE;
+  return layer_norm(x, weight, bias, y, mean, rstd, hidden, eps, param_layout, param_type, rank,
+                    shape, stream);
 }
 
 int64_t sp_layer_norm_backward_workspace(const sp_shape *shape, int32_t hidden) {
@@ -1204,7 +1235,18 @@ sp_status sp_layer_norm_backward(const void *dy, const void *x, const void *weig
                                  void *stream) {
   NvtxRange range("sp_layer_norm_backward");
   return layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, hidden,
-                             param_layout, param_type, shape, stream);
+                             param_layout, param_type, kAllShards, shape, stream);
+}
+
+sp_status sp_layer_norm_backward_rank(const void *dy, const void *x, const void *weight,
+                                      const float *mean, const float *rstd, void *dx,
+                                      void *dweight, void *dbias, void *workspace, int32_t hidden,
+                                      int32_t param_layout, int32_t param_type, int32_t rank,
+                                      const sp_shape *shape, void *stream) {
+  NvtxRange range("sp_layer_norm_backward_rank");
+  if (rank < 0) return SP_ERR_SHAPE;
+  return layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, hidden,
+                             param_layout, param_type, rank, shape, stream);
 }
 
 int64_t sp_attention_backward_workspace(const sp_shape *shape) {
