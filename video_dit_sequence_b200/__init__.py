@@ -213,8 +213,9 @@ class Shape:
         return sp_shape(self.B, self.N, self.H, self.D, self.P, float(self.scale))
 
     def c(self) -> sp_shape:
-        """The C struct (one per Shape, which the library only reads)."""
-        return self._c
+        """The C struct, the caller's own (calls that count their host time
+        pass _c, which stays as it is)."""
+        return sp_shape.from_buffer_copy(self._c)
 
 
 def padded_tokens(N: int, P: int) -> int:
@@ -698,7 +699,7 @@ def _attention_backward(name, ts, q, k, v, o, lse, do, dq, dk, dv, shape, worksp
                     (n, n, n, n, nl, n, n, n, n), (ts, ts, ts, ts, ls, ts, ts, ts, ts))
     st = _stream(stream, dev)
     ws = _workspace(workspace, need, dev, stream)
-    _call(getattr(load(), name), name, dev, *ops, ws.data_ptr(), ctypes.byref(shape.c()), st)
+    _call(getattr(load(), name), name, dev, *ops, ws.data_ptr(), ctypes.byref(shape._c), st)
 
 
 def attention_backward(q, k, v, o, lse, do, dq, dk, dv, shape: Shape, workspace=None, stream=None):
@@ -794,7 +795,7 @@ def layer_norm(x, weight, bias, y, shape: Shape, mean=None, rstd=None, eps: floa
     ops = _operands(dev, ("x", "weight", "bias", "y", "mean", "rstd"),
                     (x, weight, bias, y, mean, rstd), (bf16, dtype, dtype, bf16, f32, f32),
                     (nx, nw, nw, nx, n, n), (full, pshape, pshape, full, rows, rows))
-    _call(fn, name, dev, *ops, hidden, float(eps), layout, ptype, *more, ctypes.byref(shape.c()),
+    _call(fn, name, dev, *ops, hidden, float(eps), layout, ptype, *more, ctypes.byref(shape._c),
           _stream(stream, dev))
 
 
@@ -836,7 +837,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, shape: Shape, dweight=Non
     if dweight is not None or dbias is not None:
         ws = _workspace(workspace, layer_norm_backward_workspace(shape, hidden, rank), dev, stream)
     _call(fn, name, dev, *ops, None if ws is None else ws.data_ptr(), hidden, layout, ptype, *more,
-          ctypes.byref(shape.c()), st)
+          ctypes.byref(shape._c), st)
 
 
 SPARSE_CUBE = 64         # SP_SPARSE_CUBE
