@@ -118,3 +118,40 @@ def test_refused_way_back():
     assert not calls
     assert all(torch.equal(g, w) for g, w in zip(rank.backward_step(do, lse, copy), want))
     assert sp.device_status() == sp.SP_OK
+
+
+@pytest.mark.parametrize("eager_first", [True, False])
+def test_step_and_way_back_in_a_graph(eager_first):
+    """Captured with buffers of an earlier eager step, or its own; replayed on
+    new data, with eager steps of the same object between the replays."""
+    shape = sp.Shape(2, 150, 2, 64, 1)
+    data = [[t[0] for t in _shards(shape, 4, seed=s)] for s in (11, 12)]
+    copy = lambda send, recv: recv.copy_(send)
+    want = []
+    for q, k, v, do in data:
+        rank, lse = sp.UlyssesRank(shape), torch.empty(shape.lse_shape, device="cuda")
+        out = rank.step(q, k, v, copy, lse=lse)
+        want.append([t.clone() for t in [out] + rank.backward_step(do, lse, copy)])
+    rank, lse = sp.UlyssesRank(shape), torch.empty(shape.lse_shape, device="cuda")
+    static = [t.clone() for t in data[0]]
+
+    def there_and_back():
+        out = rank.step(*static[:3], copy, lse=lse)
+        return [out] + rank.backward_step(static[3], lse, copy)
+
+    if eager_first:
+        assert all(torch.equal(a, b) for a, b in zip(there_and_back(), want[0]))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = there_and_back()
+    for i in (0, 1, 0):
+        for s, t in zip(static, data[i]):
+            s.copy_(t)
+        for t in captured:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, want[i]))
+        assert all(torch.equal(a, b) for a, b in zip(there_and_back(), want[i]))
+    assert sp.device_status() == sp.SP_OK
