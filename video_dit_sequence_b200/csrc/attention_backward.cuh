@@ -573,7 +573,8 @@ attention_backward_kernel(const __grid_constant__ AttnBwdMaps maps,
     // products take half as long and the special-function unit bounds a tile,
     // so four of sixteen pairs go to the FMA pipe (32,760 tokens x 12 heads: 12.25
     // instead of 12.55 ms, 1,024 x 4 heads 17.8 instead of 19.2 us; six the same,
-    // eight 12.8 ms).  With D = 128 it cost 1 to 2 % at the power cap.
+    // eight 12.8 ms; the factor 2^n that keeps NaN, in the place of an addition to
+    // the exponent, 12.4).  With D = 128 it cost 1 to 2 % at the power cap.
     constexpr int kPolyPairs = D == 64 ? 4 : 0;
     auto exps = [&](uint32_t *pr, auto bias) {
 #pragma unroll

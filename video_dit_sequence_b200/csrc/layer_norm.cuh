@@ -17,7 +17,7 @@
 // elements: a team of warps takes a row, each thread V vectors of 8 columns (up
 // to 6 forward, 4 backward, where both gradient sums of every column stay in
 // registers).  One vector a thread and a block a row was bound by instructions:
-// 547 us forward and 644 us backward at 75,600 x 5,120, against 246 and 415.
+// 547 us forward and 644 us backward at 75,600 x 5,120, against 248 and 422.
 // The parameters lie in shared memory in fp32.  Each thread copies its own
 // columns of the next three rows into shared memory (cp.async, which needs no
 // synchronisation), so that some 100 KB an SM are in flight.
