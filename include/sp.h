@@ -298,7 +298,9 @@ typedef enum { SP_PARAM_BF16 = 0, SP_PARAM_FP32 = 1 } sp_param_type;
  * pages never describe the block around the attention; this is its plainest
  * reading, with the parameters either shared or per sample (a diffusion
  * transformer modulates each generation's norm by its own scale and shift).
- * fp32 arithmetic, one rounding to bf16.  The result does not depend on P.
+ * fp32 arithmetic, one rounding to bf16; the mean is held in fp32, so xh is
+ * off by up to |mean| * rstd * 2^-24 in a row whose mean is no such number.  The
+ * result does not depend on P.
  * x: device bf16 [P][B][Nl][hidden], the sequence-sharded hidden states, read
  *   only; padding slots (tokens at or past N) are not read.
  * weight, bias: device parameters of param_layout and param_type, or NULL
